@@ -409,6 +409,163 @@ pa_status pa_prefill(const pa_kv_pool* pool, const void* q, int32_t total_q,
                      int32_t* d_err, pa_stream_t stream);
 
 /*
+ * Rotary positions.  Pair i of the first rot_dim elements of a head, (x, y),
+ * becomes m (x cos a - y sin a, x sin a + y cos a) with a = position * f_i;
+ * elements behind rot_dim are kept.  Half layout: x = element i, y = element
+ * i + rot_dim / 2.  Interleaved: x = element 2 i, y = element 2 i + 1.
+ *   turns:     device uint64 [rot_dim / 2], 8-byte aligned: f_i / 2 pi modulo
+ *              one turn as a 64-bit fraction (pa_rope_turns).  position *
+ *              turns modulo 2^64 is the fraction of a turn at that position
+ *              (any int64, negative ones too), off by |position| 2^-64 turn:
+ *              under a float32's precision for positions below 2^40.
+ *   magnitude: m, a finite factor on the rotated elements (1 unless the
+ *              frequencies were scaled for a long context by a rule with one).
+ */
+typedef enum { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
+typedef struct {
+    const uint64_t* turns;
+    int32_t rot_dim;           /* even, at most the head's dimension */
+    int32_t layout;            /* pa_rope_layout */
+    float magnitude;
+} pa_rope;
+
+/*
+ * turns[i] = f_i / 2 pi, modulo one turn, as a 64-bit fraction, for n
+ * frequencies in radians a position.  Host only; host pointers.  A frequency
+ * that is not finite -> INVALID_ARG, nothing written.
+ */
+pa_status pa_rope_turns(const double* frequencies, int32_t n, uint64_t* turns);
+
+/*
+ * pa_write_kv of keys that still need their positions, with the queries of the
+ * same tokens: q_out[t] = the rotated q[t], K row of token t = the rotated
+ * k_new[t], V row = v_new[t], as pa_write_kv would write them.  Reads the
+ * three inputs where a fused projection leaves them.
+ *   q, k_new, v_new: device, token t at t * stride elements, [heads][head_dim]
+ *                    contiguous there; float32 for float32 pools, else bf16.
+ *                    Strides are at least a token's elements; a base that is
+ *                    not 16-byte aligned or a stride that is no multiple of 16
+ *                    bytes is INVALID_ARG.
+ *   positions:       device int64 [num_tokens].
+ *   slot_mapping:    device int64 [num_tokens].
+ *   q_out:           device [num_tokens][num_q_heads][head_dim], contiguous, q's
+ *                    type; may be q itself where q is contiguous, and overlaps
+ *                    no other input.  num_q_heads == 0: q and q_out unused.
+ * Rotation in float32, rounded once to the output's type; an FP8 pool's K row
+ * is quantised from the unrounded float32 values (codes and row scale as the
+ * pool description states).  A slot outside the pool sets *d_err =
+ * PA_ERR_OUT_OF_RANGE and skips that token's K and V; its query is rotated.
+ * Two tokens naming the same slot race.  num_tokens == 0 enqueues nothing.
+ * Implemented: head_dim and rot_dim multiples of 32 bytes of the input type,
+ * head_dim at most 64 times that (FP8 pools: head_dim 128); others
+ * UNSUPPORTED.  A dependent launch, as pa_write_kv.
+ */
+pa_status pa_rope_write_kv(const pa_kv_pool* pool, const pa_rope* rope, const void* q,
+                           int64_t q_stride, int32_t num_q_heads, const void* k_new,
+                           int64_t k_stride, const void* v_new, int64_t v_stride,
+                           const int64_t* positions, const int64_t* slot_mapping,
+                           int32_t num_tokens, void* q_out, int32_t* d_err, pa_stream_t stream);
+
+/*
+ * A latent pool: the paged cache of latent attention, in which a token keeps
+ * one row for all heads, [latent | rotary key].  rows is a device array
+ * [num_blocks][block_size][latent_dim + rope_dim], row-major; a token's row is
+ * at slot * (latent_dim + rope_dim).  Block tables, slots and the host
+ * allocator are those of pa_kv_pool.  bf16 only, latent_dim a multiple of 16
+ * up to 4096 and rope_dim one up to 1024 (others UNSUPPORTED); 16-byte aligned.
+ */
+typedef struct {
+    void* rows;
+    int32_t num_blocks;
+    int32_t block_size;
+    int32_t latent_dim;
+    int32_t rope_dim;
+    int32_t dtype;             /* PA_DTYPE_BF16 */
+} pa_latent_pool;
+
+/*
+ * Scatter write of new tokens into a latent pool: the row at slot_mapping[t]
+ * becomes [latent[t] | rotated k_rope[t]], and, for num_q_heads > 0, the last
+ * rope_dim elements of q[t][h] become the rotated q_rope[t][h]; the absorbed
+ * part of q, its first latent_dim elements, is left as it is.
+ *   latent, k_rope: device bf16, token t at t * stride elements.
+ *   q_rope:         device bf16, head h of token t at t * q_rope_stride +
+ *                   h * q_rope_head_stride elements.
+ *   q:              device bf16 [num_tokens][num_q_heads][latent_dim + rope_dim].
+ *                   Overlaps no input.
+ * All bases and strides are multiples of 16 bytes (else INVALID_ARG);
+ * rope->rot_dim == rope_dim.  Rotation in float32, rounded once; the latent
+ * part is copied bit for bit.  Slots and errors as pa_rope_write_kv.  A
+ * dependent launch, as pa_write_kv.
+ */
+pa_status pa_write_latent(const pa_latent_pool* pool, const pa_rope* rope, const void* latent,
+                          int64_t latent_stride, const void* k_rope, int64_t k_rope_stride,
+                          const int64_t* positions, const int64_t* slot_mapping,
+                          int32_t num_tokens, const void* q_rope, int64_t q_rope_stride,
+                          int64_t q_rope_head_stride, int32_t num_q_heads, void* q, int32_t* d_err,
+                          pa_stream_t stream);
+
+/* pa_copy_blocks for a latent pool: block dst[i] becomes a copy of src[i]. */
+pa_status pa_copy_latent_blocks(const pa_latent_pool* pool, const int32_t* src, const int32_t* dst,
+                                int32_t n, int32_t* d_err, pa_stream_t stream);
+
+/*
+ * Latent attention in the absorbed form, one query token a sequence:
+ *   out[s][g] = sum_j softmax_j(scale * q[s][g] . row_j) latent_j  over j < n,
+ * n = context_lens[s], row_j the whole row of token j and latent_j its first
+ * latent_dim elements.  One row serves every head, as key and as value.
+ *   q:            device bf16 [num_seqs][num_q_heads][latent_dim + rope_dim].
+ *   out:          device bf16 [num_seqs][num_q_heads][latent_dim].
+ *   workspace:    device, >= pa_decode_latent_workspace_bytes(...) bytes, 16-byte
+ *                 aligned; may be NULL when that is 0.  Holds the partials of
+ *                 contexts that are split; calls that may overlap need one each.
+ * block_tables, context_lens (0 leaves out[s] untouched), max_context, and
+ * errors as pa_decode; a sequence whose every page is outside the pool gets
+ * zeros.  Rows past a context's end are never used, whatever they hold.
+ * Implemented: latent_dim 128, 256, 384 or 512, rope_dim 16, 32, 48 or 64,
+ * block size a power of two in [8, 128], num_q_heads <= 128, at most 65535
+ * sequences, num_blocks * block_size < 2^31; others UNSUPPORTED.
+ * Arithmetic: products on bf16 operands with float32 accumulation; softmax
+ * statistics and accumulators in float32; the probabilities enter the second
+ * product as bf16 (their sum is taken of the rounded values), and the output
+ * is rounded once, so the result is as exact as a bf16 output can show.
+ */
+pa_status pa_decode_latent_workspace_bytes(const pa_latent_pool* pool, int32_t num_seqs,
+                                           int32_t num_q_heads, int32_t max_context, size_t* bytes);
+pa_status pa_decode_latent(const pa_latent_pool* pool, const void* q, int32_t num_q_heads,
+                           const int32_t* block_tables, int32_t max_blocks_per_seq,
+                           const int32_t* context_lens, int32_t num_seqs, int32_t max_context,
+                           float scale, void* out, void* workspace, size_t workspace_bytes,
+                           int32_t* d_err, pa_stream_t stream);
+
+/*
+ * The same for several new tokens a sequence (a chunk of a prompt behind its
+ * cached part, drafted tokens to be checked): sequence s has the queries
+ * q[cu_seqlens_q[s] .. cu_seqlens_q[s+1]), whose rows are already written; new
+ * token i is at position context_lens[s] - n_new + i and sees positions 0 to
+ * its own (causal != 0) or all context_lens[s].
+ *   q:    device bf16 [total_q][num_q_heads][latent_dim + rope_dim].
+ *   out:  device bf16 [total_q][num_q_heads][latent_dim].
+ * Sequences with no new token are skipped, and rows of q behind the last
+ * sequence leave out as it is.  Device errors: offsets that descend or leave
+ * [0, total_q] set OUT_OF_RANGE and skip the sequence; n_new > context_lens[s]
+ * sets INVALID_ARG and skips it; n_new > max_q_len sets OUT_OF_RANGE and leaves
+ * the tokens behind max_q_len; positions from max_context on are not seen and
+ * set OUT_OF_RANGE.  Workspace, limits, errors and arithmetic as
+ * pa_decode_latent; total_q * num_q_heads < 2^31.
+ */
+pa_status pa_prefill_latent_workspace_bytes(const pa_latent_pool* pool, int32_t num_seqs,
+                                            int32_t num_q_heads, int32_t total_q,
+                                            int32_t max_q_len, int32_t max_context, size_t* bytes);
+pa_status pa_prefill_latent(const pa_latent_pool* pool, const void* q, int32_t total_q,
+                            int32_t num_q_heads, const int32_t* cu_seqlens_q,
+                            const int32_t* context_lens, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, int32_t num_seqs, int32_t max_q_len,
+                            int32_t max_context, float scale, int32_t causal, void* out,
+                            void* workspace, size_t workspace_bytes, int32_t* d_err,
+                            pa_stream_t stream);
+
+/*
  * Host block allocator: refcounts, free list, fork and copy-on-write tail
  * (P2 "引用计数与尾块 COW" and "生命周期与所有权"; P1 §5).  A handle is not
  * thread-safe.  Tables are caller-owned host int32 arrays; *n is their

@@ -9,11 +9,14 @@ computing anything another way.
 Entry points (same names as the C ABI, without the ``pa_`` prefix):
 ``write_kv``, ``copy_blocks``, ``decode``, ``prefill``, ``physical_slot``,
 ``slot_mapping``, ``page_size_bytes``, ``decode_partition_tokens``,
-``decode_workspace_bytes`` and the host block ``Allocator``.
+``decode_workspace_bytes`` and the host block ``Allocator``; rotary positions
+(``Rope``, ``rope_write_kv``) and the latent cache (``LatentPool``,
+``write_latent``, ``copy_latent_blocks``, ``decode_latent``, ``prefill_latent``).
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence
 
@@ -45,6 +48,9 @@ EXPORTED = [
     "pa_decode_window_workspace_bytes", "pa_decode_window", "pa_decode_shared_workspace_bytes",
     "pa_decode_shared",
     "pa_prefill",
+    "pa_rope_turns", "pa_rope_write_kv", "pa_write_latent", "pa_copy_latent_blocks",
+    "pa_decode_latent_workspace_bytes", "pa_decode_latent", "pa_prefill_latent_workspace_bytes",
+    "pa_prefill_latent",
     "pa_alloc_create", "pa_alloc_destroy", "pa_alloc_append", "pa_alloc_fork",
     "pa_alloc_writable_tail", "pa_alloc_reserve", "pa_alloc_release", "pa_alloc_refcount",
     "pa_alloc_num_free",
@@ -63,6 +69,17 @@ class pa_kv_pool(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p)]
+
+
+class pa_rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
+class pa_latent_pool(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("num_blocks", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -107,6 +124,15 @@ def lib() -> ctypes.CDLL:
         "pa_decode_shared_workspace_bytes": ([P, i32, i32, i32, i32, P], i32),
         "pa_decode_shared": ([P, P, i32, P, i32, P, i32, i32, P, P, f32, i32, P, P, sz, P, P], i32),
         "pa_prefill": ([P, P, i32, i32, P, P, P, i32, i32, i32, i32, f32, i32, P, P, P], i32),
+        "pa_rope_turns": ([P, i32, P], i32),
+        "pa_rope_write_kv": ([P, P, P, i64, i32, P, i64, P, i64, P, P, i32, P, P, P], i32),
+        "pa_write_latent": ([P, P, P, i64, P, i64, P, P, i32, P, i64, i64, i32, P, P, P], i32),
+        "pa_copy_latent_blocks": ([P, P, P, i32, P, P], i32),
+        "pa_decode_latent_workspace_bytes": ([P, i32, i32, i32, P], i32),
+        "pa_decode_latent": ([P, P, i32, P, i32, P, i32, i32, f32, P, P, sz, P, P], i32),
+        "pa_prefill_latent_workspace_bytes": ([P, i32, i32, i32, i32, i32, P], i32),
+        "pa_prefill_latent": ([P, P, i32, i32, P, P, P, i32, i32, i32, i32, f32, i32, P, P, sz, P, P],
+                              i32),
         "pa_alloc_create": ([i32, P, P], i32),
         "pa_alloc_destroy": ([P], None),
         "pa_alloc_append": ([P, P, P, i32], i32),
@@ -500,6 +526,381 @@ def prefill(pool: KVPool, q: torch.Tensor, cu_seqlens_q: torch.Tensor, context_l
                             int(context_lens.shape[0]), int(max_q_len), int(max_context),
                             float(scale), 1 if causal else 0, _ptr(out), _ptr(d_err),
                             _stream(stream)), "pa_prefill")
+    return out
+
+
+# --------------------------------------------------------------------------- rotary positions
+class Rope:
+    """Rotary positions: the frequencies of rot_dim / 2 pairs, on one device.
+
+    Pair i turns by position * f_i, f_i = base^(-2 i / rot_dim).  layout "half"
+    pairs element i with i + rot_dim / 2, "interleaved" 2 i with 2 i + 1.
+    scaling stretches the frequencies for contexts `factor` times the trained one:
+
+    * "linear": f_i / factor (positions interpolated);
+    * "ntk": the base becomes base * factor^(rot_dim / (rot_dim - 2)), so the
+      slowest pair is stretched by factor and the fastest not at all;
+    * "by_parts" (YaRN, Peng et al. 2023, sections 3.2 to 3.4): with r_i the turns
+      that pair i makes over original_context, g_i = clamp((r_i - slow) /
+      (fast - slow), 0, 1), f_i becomes g_i f_i + (1 - g_i) f_i / factor, and
+      rotated elements are multiplied by 0.1 ln(factor) + 1.
+
+    frequencies (radians a position, rot_dim / 2 values) and magnitude replace
+    the computed ones.
+    """
+
+    SCALINGS = ("none", "linear", "ntk", "by_parts")
+    LAYOUTS = ("half", "interleaved")
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, layout: str = "half",
+                 scaling: str = "none", factor: float = 1.0,
+                 original_context: Optional[int] = None, fast: float = 32.0, slow: float = 1.0,
+                 frequencies=None, magnitude: Optional[float] = None, device="cuda"):
+        if layout not in self.LAYOUTS:
+            raise ValueError("layout must be one of %s" % (self.LAYOUTS,))
+        if scaling not in self.SCALINGS:
+            raise ValueError("scaling must be one of %s" % (self.SCALINGS,))
+        self.rot_dim, self.layout = int(rot_dim), layout
+        if self.rot_dim <= 0 or self.rot_dim % 2:
+            raise ValueError("rot_dim must be even and positive")
+        if not (base > 0 and math.isfinite(base) and factor >= 1 and math.isfinite(factor)):
+            raise ValueError("base must be positive and factor at least 1, both finite")
+        m = 1.0
+        if frequencies is not None:
+            if scaling != "none":
+                raise ValueError("frequencies are given already scaled: scaling must be 'none'")
+            f = np.array(frequencies, dtype=np.float64)
+            if f.shape != (self.rot_dim // 2,):
+                raise ValueError("frequencies must hold rot_dim / 2 = %d values" % (self.rot_dim // 2))
+        else:
+            if scaling == "ntk":
+                if self.rot_dim < 4:
+                    raise ValueError("ntk scaling needs rot_dim >= 4")
+                base = base * factor ** (self.rot_dim / (self.rot_dim - 2))
+            f = base ** (-2.0 * np.arange(self.rot_dim // 2) / self.rot_dim)
+            if scaling == "linear":
+                f = f / factor
+            elif scaling == "by_parts":
+                if original_context is None or original_context <= 0 or not fast > slow:
+                    raise ValueError("by_parts scaling needs original_context > 0 and fast > slow")
+                g = np.clip((original_context * f / (2 * math.pi) - slow) / (fast - slow), 0.0, 1.0)
+                f = g * f + (1 - g) * f / factor
+                m = 0.1 * math.log(factor) + 1.0
+        self.magnitude = float(m if magnitude is None else magnitude)
+        if not (np.isfinite(f).all() and math.isfinite(self.magnitude)):
+            raise ValueError("frequencies and magnitude must be finite")
+        self.frequencies = f
+        turns = np.empty(len(f), np.uint64)
+        _check(lib().pa_rope_turns(f.ctypes.data, len(f), turns.ctypes.data), "pa_rope_turns")
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.device = self.turns.device
+        self._c = pa_rope(self.turns.data_ptr(), self.rot_dim, self.LAYOUTS.index(layout),
+                          self.magnitude)
+        self.c = ctypes.byref(self._c)
+
+
+def _need_heads(t: torch.Tensor, name: str, dtype, device, tokens: int, heads: int, dim: int):
+    """t [tokens][heads][dim], a token's elements contiguous; returns the token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s must live on %s, got %s" % (name, device, t.device))
+    if t.dim() != 3 or t.shape != (tokens, heads, dim):
+        raise ValueError("%s must have shape %s, got %s"
+                         % (name, (tokens, heads, dim), tuple(t.shape)))
+    st, sh, sd = t.stride()
+    if (dim > 1 and sd != 1) or (heads > 1 and sh != dim):
+        raise ValueError("each token of %s must be contiguous" % name)
+    return st if tokens > 1 else heads * dim
+
+
+class _On:
+    """The device and stream of a call: `stream`, or the current one of the tensors' device."""
+
+    __slots__ = ("guard", "handle", "stream")
+
+    def __init__(self, device, stream):
+        self.guard = None
+        if device.type == "cuda" and device.index is not None \
+                and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.stream = stream
+        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def made(self, t):
+        """A tensor made by the call itself: its memory waits for `stream` too before it is reused."""
+        if t is not None and self.stream is not None:
+            t.record_stream(self.stream)
+        return t
+
+
+def rope_write_kv(pool: KVPool, q: Optional[torch.Tensor], k_new: torch.Tensor,
+                  v_new: torch.Tensor, positions: torch.Tensor, slot_mapping: torch.Tensor,
+                  rope: Rope, q_out: Optional[torch.Tensor] = None,
+                  d_err: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Rotate q [T][H_q][D] and k_new [T][H_kv][D] at positions [T] (int64) and write the
+    rotated K and v_new to the pool at slot_mapping [T] (int64); returns the rotated q.
+
+    q, k_new and v_new may be slices of one projection (any token stride).  q None
+    writes K and V alone; q_out may be q.
+    """
+    T = int(slot_mapping.shape[0])
+    dev, io, D = pool.device, pool.io_dtype, pool.head_dim
+    ks = _need_heads(k_new, "k_new", io, dev, T, pool.num_kv_heads, D)
+    vs = _need_heads(v_new, "v_new", io, dev, T, pool.num_kv_heads, D)
+    _need(positions, "positions", torch.int64, dev)
+    _need(slot_mapping, "slot_mapping", torch.int64, dev)
+    _need_shape(positions, "positions", (T,))
+    _need_shape(slot_mapping, "slot_mapping", (T,))
+    _need_err(d_err, dev)
+    _need_rope(rope, dev)
+    Hq = qs = 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a tensor [T][H_q][D]")
+        Hq = int(q.shape[1])
+        qs = _need_heads(q, "q", io, dev, T, Hq, D)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if q_out is not None:
+        _need(q_out, "q_out", io, dev)
+        _need_shape(q_out, "q_out", (T, Hq, D))
+    with _On(dev, stream) as on:
+        if q is not None and q_out is None:
+            q_out = on.made(torch.empty((T, Hq, D), dtype=io, device=dev))
+        _check(lib().pa_rope_write_kv(pool.c, rope.c, q.data_ptr() if Hq else None, qs, Hq,
+                                      k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+                                      positions.data_ptr(), slot_mapping.data_ptr(), T,
+                                      q_out.data_ptr() if Hq else None,
+                                      None if d_err is None else d_err.data_ptr(), on.handle),
+               "pa_rope_write_kv")
+    return q_out
+
+
+def _need_rope(rope, device):
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    if rope.device != device:
+        raise ValueError("rope must live on %s, got %s" % (device, rope.device))
+
+
+# --------------------------------------------------------------------------- latent cache
+class LatentPool:
+    """Block pool of a latent cache: rows [num_blocks][block_size][latent_dim + rope_dim], bf16.
+
+    A token keeps one row for all heads: its latent vector, key and value at once
+    in the absorbed form, and a rotary key behind it.
+    """
+
+    def __init__(self, num_blocks: int, block_size: int, latent_dim: int, rope_dim: int,
+                 dtype: torch.dtype = torch.bfloat16, device="cuda", rows=None):
+        if dtype != torch.bfloat16:
+            raise TypeError("latent pool dtype must be bfloat16")
+        self.num_blocks, self.block_size = int(num_blocks), int(block_size)
+        self.latent_dim, self.rope_dim = int(latent_dim), int(rope_dim)
+        self.width = self.latent_dim + self.rope_dim
+        self.dtype = dtype
+        shape = (self.num_blocks, self.block_size, self.width)
+        self.rows = torch.empty(shape, dtype=dtype, device=device) if rows is None else rows
+        _need(self.rows, "rows", dtype)
+        _need_shape(self.rows, "rows", shape)
+        self.device = self.rows.device
+        self._c = pa_latent_pool(self.rows.data_ptr(), self.num_blocks, self.block_size,
+                                 self.latent_dim, self.rope_dim, DTYPE_BF16)
+        self.c = ctypes.byref(self._c)
+
+    def poison(self):
+        """Fill the pool with NaN bit patterns (all bytes 0xFF)."""
+        self.rows.view(torch.uint8).fill_(0xFF)
+        return self
+
+
+def write_latent(pool: LatentPool, latent: torch.Tensor, k_rope: torch.Tensor,
+                 positions: torch.Tensor, slot_mapping: torch.Tensor, rope: Rope,
+                 q_rope: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                 d_err: Optional[torch.Tensor] = None, stream=None):
+    """Write latent [T][latent_dim] and the rotated k_rope [T][rope_dim] to the pool at
+    slot_mapping [T] (int64), and the rotated q_rope [T][H][rope_dim] behind the absorbed
+    part of q [T][H][latent_dim + rope_dim] (both or neither; returns q).
+
+    latent, k_rope and q_rope may be slices of wider projections (any token and head
+    stride that is a multiple of 16 bytes).
+    """
+    T, dev = int(slot_mapping.shape[0]), pool.device
+    for t, name, dim in ((latent, "latent", pool.latent_dim), (k_rope, "k_rope", pool.rope_dim)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError("%s must be a tensor [T][%d]" % (name, dim))
+    ls = _need_heads(latent.unsqueeze(1), "latent", pool.dtype, dev, T, 1, pool.latent_dim)
+    ks = _need_heads(k_rope.unsqueeze(1), "k_rope", pool.dtype, dev, T, 1, pool.rope_dim)
+    _need(positions, "positions", torch.int64, dev)
+    _need(slot_mapping, "slot_mapping", torch.int64, dev)
+    _need_shape(positions, "positions", (T,))
+    _need_shape(slot_mapping, "slot_mapping", (T,))
+    _need_err(d_err, dev)
+    _need_rope(rope, dev)
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q come together")
+    H = qs = qh = 0
+    if q is not None:
+        _need(q, "q", pool.dtype, dev)
+        if q.dim() != 3:
+            raise ValueError("q must be [T][H][%d]" % pool.width)
+        H = int(q.shape[1])
+        _need_shape(q, "q", (T, H, pool.width))
+        if not isinstance(q_rope, torch.Tensor) or q_rope.dtype != pool.dtype:
+            raise TypeError("q_rope must be a %s tensor" % pool.dtype)
+        if q_rope.device != dev:
+            raise ValueError("q_rope must live on %s, got %s" % (dev, q_rope.device))
+        _need_shape(q_rope, "q_rope", (T, H, pool.rope_dim))
+        if q_rope.stride(2) != 1 and pool.rope_dim > 1:
+            raise ValueError("each head of q_rope must be contiguous")
+        qh = q_rope.stride(1) if H > 1 else pool.rope_dim
+        qs = q_rope.stride(0) if T > 1 else max((H - 1) * qh + pool.rope_dim, 0)
+    with _On(dev, stream) as on:
+        _check(lib().pa_write_latent(pool.c, rope.c, latent.data_ptr(), ls, k_rope.data_ptr(), ks,
+                                     positions.data_ptr(), slot_mapping.data_ptr(), T,
+                                     q_rope.data_ptr() if H else None, qs, qh, H,
+                                     q.data_ptr() if H else None,
+                                     None if d_err is None else d_err.data_ptr(), on.handle),
+               "pa_write_latent")
+    return q
+
+
+def copy_latent_blocks(pool: LatentPool, src: torch.Tensor, dst: torch.Tensor,
+                       d_err: Optional[torch.Tensor] = None, stream=None):
+    """Block copy dst[i] <- src[i] (int32 device tensors) in a latent pool."""
+    _need(src, "src", torch.int32, pool.device)
+    _need(dst, "dst", torch.int32, pool.device)
+    if src.shape != dst.shape or src.dim() != 1:
+        raise ValueError("src and dst must be 1-D of equal length")
+    _need_err(d_err, pool.device)
+    with _On(pool.device, stream) as on:
+        _check(lib().pa_copy_latent_blocks(pool.c, src.data_ptr(), dst.data_ptr(),
+                                           int(src.shape[0]),
+                                           None if d_err is None else d_err.data_ptr(), on.handle),
+               "pa_copy_latent_blocks")
+
+
+def decode_latent_workspace_bytes(pool: LatentPool, num_seqs: int, num_q_heads: int,
+                                  max_context: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().pa_decode_latent_workspace_bytes(pool.c, num_seqs, num_q_heads, max_context,
+                                                  ctypes.byref(out)),
+           "pa_decode_latent_workspace_bytes")
+    return out.value
+
+
+def prefill_latent_workspace_bytes(pool: LatentPool, num_seqs: int, num_q_heads: int, total_q: int,
+                                   max_q_len: int, max_context: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().pa_prefill_latent_workspace_bytes(pool.c, num_seqs, num_q_heads, total_q,
+                                                   max_q_len, max_context, ctypes.byref(out)),
+           "pa_prefill_latent_workspace_bytes")
+    return out.value
+
+
+def decode_latent_workspace(pool: LatentPool, num_seqs: int, num_q_heads: int,
+                            max_context: int) -> Optional[torch.Tensor]:
+    """A workspace for decode_latent (reusable by every later call of the shape), or None."""
+    n = decode_latent_workspace_bytes(pool, num_seqs, num_q_heads, max_context)
+    return torch.empty(n, dtype=torch.uint8, device=pool.device) if n > 0 else None
+
+
+def prefill_latent_workspace(pool: LatentPool, num_seqs: int, num_q_heads: int, total_q: int,
+                             max_q_len: int, max_context: int) -> Optional[torch.Tensor]:
+    """A workspace for prefill_latent (reusable by every later call of the shape), or None."""
+    n = prefill_latent_workspace_bytes(pool, num_seqs, num_q_heads, total_q, max_q_len, max_context)
+    return torch.empty(n, dtype=torch.uint8, device=pool.device) if n > 0 else None
+
+
+def _need_latent_q(pool, q, block_tables, context_lens, out):
+    _need(q, "q", pool.dtype, pool.device)
+    _need(block_tables, "block_tables", torch.int32, pool.device)
+    _need(context_lens, "context_lens", torch.int32, pool.device)
+    if q.dim() != 3 or q.shape[2] != pool.width:
+        raise ValueError("q must be [T][H][%d], got %s" % (pool.width, tuple(q.shape)))
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens must be 1-D")
+    B = int(context_lens.shape[0])
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [%d][max_blocks], got %s"
+                         % (B, tuple(block_tables.shape)))
+    T, H = int(q.shape[0]), int(q.shape[1])
+    if out is not None:
+        _need(out, "out", pool.dtype, pool.device)
+        _need_shape(out, "out", (T, H, pool.latent_dim))
+    return T, H, B
+
+
+def decode_latent(pool: LatentPool, q: torch.Tensor, block_tables: torch.Tensor,
+                  context_lens: torch.Tensor, max_context: int, scale: float,
+                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  d_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Latent attention of one token a sequence, absorbed form; returns out [B][H][latent_dim] bf16.
+
+    q: [B][H][latent_dim + rope_dim], the query absorbed into the latent space with the
+    rotated part behind it (write_latent).  workspace: decode_latent_workspace(); one is
+    made where it is missing or too small.
+    """
+    T, H, B = _need_latent_q(pool, q, block_tables, context_lens, out)
+    if T != B:
+        raise ValueError("q must hold one token a sequence: %d, got %d" % (B, T))
+    _need_workspace(workspace, pool.device)
+    _need_err(d_err, pool.device)
+    need = decode_latent_workspace_bytes(pool, B, H, int(max_context))
+    with _On(pool.device, stream) as on:
+        if out is None:
+            out = on.made(torch.empty((T, H, pool.latent_dim), dtype=pool.dtype, device=pool.device))
+        have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        if have < need:
+            workspace, have = on.made(torch.empty(need, dtype=torch.uint8, device=pool.device)), need
+        _check(lib().pa_decode_latent(pool.c, q.data_ptr(), H, block_tables.data_ptr(),
+                                      int(block_tables.shape[1]), context_lens.data_ptr(), B,
+                                      int(max_context), float(scale), out.data_ptr(),
+                                      workspace.data_ptr() if have else None, have,
+                                      None if d_err is None else d_err.data_ptr(), on.handle),
+               "pa_decode_latent")
+    return out
+
+
+def prefill_latent(pool: LatentPool, q: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                   context_lens: torch.Tensor, block_tables: torch.Tensor, max_q_len: int,
+                   max_context: int, scale: float, causal: bool = True,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   d_err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Latent attention of several new tokens a sequence, absorbed form; returns out
+    [T][H][latent_dim] bf16.  q: [T][H][latent_dim + rope_dim], sequence s at
+    cu_seqlens_q[s] .. cu_seqlens_q[s + 1]; its tokens' rows are already written."""
+    T, H, B = _need_latent_q(pool, q, block_tables, context_lens, out)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, pool.device)
+    _need_shape(cu_seqlens_q, "cu_seqlens_q", (B + 1,))
+    _need_workspace(workspace, pool.device)
+    _need_err(d_err, pool.device)
+    need = prefill_latent_workspace_bytes(pool, B, H, T, int(max_q_len), int(max_context))
+    with _On(pool.device, stream) as on:
+        if out is None:
+            out = on.made(torch.empty((T, H, pool.latent_dim), dtype=pool.dtype, device=pool.device))
+        have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        if have < need:
+            workspace, have = on.made(torch.empty(need, dtype=torch.uint8, device=pool.device)), need
+        _check(lib().pa_prefill_latent(pool.c, q.data_ptr(), T, H, cu_seqlens_q.data_ptr(),
+                                       context_lens.data_ptr(), block_tables.data_ptr(),
+                                       int(block_tables.shape[1]), B, int(max_q_len),
+                                       int(max_context), float(scale), 1 if causal else 0,
+                                       out.data_ptr(), workspace.data_ptr() if have else None, have,
+                                       None if d_err is None else d_err.data_ptr(), on.handle),
+               "pa_prefill_latent")
     return out
 
 

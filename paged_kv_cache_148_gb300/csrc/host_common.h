@@ -37,6 +37,18 @@ inline pa_status check_pool(const pa_kv_pool* p) {
     return PA_OK;
 }
 
+inline pa_status check_latent_pool(const pa_latent_pool* p) {
+    if (p == nullptr || p->rows == nullptr) return PA_ERR_INVALID_ARG;
+    if (p->num_blocks <= 0 || p->block_size <= 0 || p->latent_dim <= 0 || p->rope_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (p->dtype != PA_DTYPE_F32 && p->dtype != PA_DTYPE_BF16 && p->dtype != PA_DTYPE_FP8_E4M3)
+        return PA_ERR_INVALID_ARG;
+    if (p->dtype != PA_DTYPE_BF16 || p->latent_dim % 16 != 0 || p->rope_dim % 16 != 0 ||
+        p->latent_dim > 4096 || p->rope_dim > 1024)
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
 // Status of the launch just made (cudaGetLastError).
 inline pa_status launch_status() {
     cudaError_t e = cudaGetLastError();
