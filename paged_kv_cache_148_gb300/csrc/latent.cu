@@ -1,112 +1,805 @@
 // pa_decode_latent and pa_prefill_latent: attention over a latent pool in the
-// absorbed form.  A token's row is [latent | rotary key]; every query head
-// carries [absorbed query | rotated query] of the same width, so
-//   s_j = scale * q . row_j,   out = sum_j softmax(s)_j latent_j.
+// absorbed form, on the 5th-generation tensor cores.
+//
+// A token's row is [latent | rotary key] and serves every head, as key whole and
+// as value by its latent part:  s_j = scale * q . row_j,
+// out = sum_j softmax(s)_j latent_j.
+//
+// One unit of work is up to 64 query rows (token, head) of one sequence against
+// a stretch of its context in tiles of 64 tokens.  A staged tile is used twice
+// from the same shared memory:
+//   S   [64 rows x 64 tokens] = Q (A, K-major)  x tile (B, K-major),
+//   O^T [dims x rows]        += tile^T (A, MN-major, 128 dims an MMA) x P^T (B, K-major).
+// The second product is transposed because its accumulator then has one TMEM
+// column a query row and 128 dims a lane block: 512 dims x 64 rows take 256
+// columns and leave room for two S buffers, where O with rows as lanes would
+// fill all 512.
+//
+// Roles (192 threads, one CTA per SM):
+//   warp 0     TMA producer: Q of a unit; the tiles as boxes of one page x 64
+//              elements (128-byte swizzle) through the block table, into a
+//              ring of 128-dim pairs and a ring of rotary blocks.
+//   warp 1     MMA issuer: S of tile j + 1 before O^T of tile j, so that the
+//              softmax of one tile runs beside the products of others.
+//   warps 2-5  softmax of S (each warp 16 rows, a row over 4 lanes), base 2;
+//              P as bf16 into shared memory; the epilogue.
+//
+// All units' tiles of a call form one line, cut into equal stretches, one a CTA
+// (a CTA group of 2 for 65 to 128 heads of a decode: the siblings take half of
+// the heads each and stream the same tiles, so that one of them hits in L2).
+// A unit whose tiles lie in one stretch is written at once; the parts of a cut
+// one go to the workspace as (max, sum, unnormalised O) in float32, and a second
+// kernel joins them.
+//
+// The running reference of a row's scores moves only when its maximum grew by
+// more than 2^16 (bf16 has float32's range, so P loses nothing by it): the
+// rescaling of O^T, which takes all four warps, is then rare.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "host_common.h"
 #include "rope.cuh"
+#include "tcgen05.cuh"
 
 namespace pa {
+namespace lat {
 
-struct LatentParams {
-    const uint16_t* rows;
-    int32_t num_blocks, block_size, latent_dim, rope_dim;
-    const uint16_t* q;
+constexpr int kTok = 64;             // tokens of a tile
+constexpr int kBlock = kTok * 128;   // bytes of 64 tokens x 64 elements
+constexpr int kPair = 2 * kBlock;
+constexpr int kThreads = 192;
+constexpr int kMaxPairs = 12;        // ring slots
+constexpr int kMaxRope = 3;
+constexpr float kRescale = 16.0f;
+constexpr int kBarBytes = 1536;
+constexpr int kSmemLimit = 232448;   // 227 KB
+
+struct Params {
+    int32_t num_blocks, log2_bp, latent_dim, rope_dim;
     int32_t heads;
     const int32_t *starts, *lens, *tables;  // starts: null for one query a sequence
     int32_t max_blocks, seqs, max_q, total_q, max_context, causal;
     float scale_log2;
+    int32_t siblings;                // CTAs that share a unit's tiles (decode: 1 or 2)
+    int32_t unit_rows;               // rows of a unit
+    int32_t R;                       // unit_rows rounded up to 16: N of the second product
+    int32_t groups;                  // stretches
+    int32_t min_tiles;               // least tiles a stretch
+    int32_t pair_slots, rope_slots;
+    int32_t off_p, off_rope, off_pairs, off_bars;  // shared memory
     uint16_t* out;
+    int4* meta;                      // [groups * siblings]: parts of the unit cut behind this stretch
+    float2* stats;                   // [2 * groups * siblings][R]: (max, sum) of a part's rows
+    float* parts;                    // [2 * groups * siblings][R][latent_dim]
     int32_t* d_err;
 };
 
-// One warp a (query, head) row, online softmax over the tokens one by one; lane
-// l holds elements 2l + 64i, 2l + 64i + 1.
-constexpr int kLatentPairs = 9;  // up to 576 elements a row
+struct Bars {
+    uint64_t q_full, q_empty, o_free;
+    uint64_t pair_full[kMaxPairs], pair_empty[kMaxPairs];
+    uint64_t rope_full[kMaxRope], rope_empty[kMaxRope];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint32_t tmem_base;
+    int32_t abort;
+    uint32_t valid[4];               // pages of a tile that were loaded, by tile mod 4
+    float factor[64];                // rescaling factors of the rows
+    float inv[2][64];                // one over the rows' sums, by unit mod 2
+    int64_t scan[8];
+    int64_t at, per;
+    int32_t seq;
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier area");
 
-__global__ void __launch_bounds__(128) latent_rows_kernel(const LatentParams p) {
-    const int s = blockIdx.y, lane = threadIdx.x & 31;
-    const int start = p.starts ? p.starts[s] : s;
-    const int new_q = p.starts ? p.starts[s + 1] - start : 1;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int n = p.lens[s];
-    if (p.starts && (start < 0 || new_q < 0 || new_q > p.total_q - start)) {
-        set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
-        return;
+// A warp's bounded wait.  Once one has run out the CTA winds down: every later
+// wait that would block returns at once.
+PA_DEVICE bool wait_warp(uint64_t* bar, uint32_t parity, Bars* b, int32_t* d_err) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        while (!(ok = mbar_try_wait(bar, parity))) {
+            if (*(volatile int32_t*)&b->abort) break;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                set_error(d_err, PA_ERR_TIMEOUT);
+                *(volatile int32_t*)&b->abort = 1;
+                break;
+            }
+        }
     }
-    if (new_q == 0 || (!p.starts && n <= 0)) return;
-    if (n < new_q) {
-        set_error(p.d_err, PA_ERR_INVALID_ARG);
-        return;
+    return __all_sync(0xffffffffu, ok);
+}
+
+PA_DEVICE void named_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+PA_DEVICE bool named_any(int id, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(id), "r"((uint32_t)x) : "memory");
+    return r != 0;
+}
+
+// 16 lanes x 64 columns: thread t gets, for column group i of 8, rows t / 4 (regs
+// 4i, 4i + 1) and t / 4 + 8 (4i + 2, 4i + 3), columns 8i + 2 (t % 4) and the next.
+PA_DEVICE void tmem_ld_16x256_x8(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+PA_DEVICE void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+PA_DEVICE void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+          "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+          "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// ---------------------------------------------------------------- the line of tiles
+// A sequence's units and the tiles that the line holds for each.  With a causal
+// mask unit u needs ceil(seen / 64) tiles, seen growing with u; the line gives it
+// first + u / heads, at least as many (at most two more) and with a sum in
+// closed form, so that a stretch finds its place without walking the units.
+struct Seq {
+    int32_t start, fresh, n;   // first query token; query tokens; context
+    int32_t units, first, step;  // tiles of unit u: first + u / step (step 0: first)
+
+    PA_DEVICE int64_t before(int64_t u) const {
+        if (step == 0) return u * first;
+        const int64_t k = u / step;
+        return u * first + step * (k * (k - 1) / 2) + k * (u - k * step);
     }
-    if (n > p.max_context || new_q > p.max_q) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
-    if (r >= (int64_t)min(new_q, p.max_q) * p.heads) return;
-    const int i = (int)(r / p.heads);
-    const int seen = min(p.causal ? n - new_q + i + 1 : n, p.max_context);
-    const int width = p.latent_dim + p.rope_dim;
-    const int64_t row = (int64_t)start * p.heads + r;
-    const uint32_t* q = (const uint32_t*)(p.q + row * width);
-    float2 qf[kLatentPairs], acc[kLatentPairs];
-#pragma unroll
-    for (int c = 0; c < kLatentPairs; ++c) {
-        const int e = 2 * lane + 64 * c;
-        const uint32_t w = e < width ? q[e >> 1] : 0;
-        qf[c] = make_float2(bf16_lo(w), bf16_hi(w));
-        acc[c] = make_float2(0.f, 0.f);
+};
+
+template <bool REPORT>
+PA_DEVICE Seq read_seq(const Params& p, int s) {
+    Seq q;
+    q.units = q.first = q.step = 0;
+    q.start = p.starts ? __ldg(p.starts + s) : s;
+    q.fresh = p.starts ? __ldg(p.starts + s + 1) - q.start : 1;
+    q.n = __ldg(p.lens + s);
+    if (p.starts && (q.start < 0 || q.fresh < 0 || q.fresh > p.total_q - q.start)) {
+        if (REPORT) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
+        return q;
     }
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < seen; ++j) {
-        const int e = j / p.block_size;
-        const int blk = e < p.max_blocks ? p.tables[(int64_t)s * p.max_blocks + e] : -1;
-        if (blk < 0 || blk >= p.num_blocks) {
-            set_error(p.d_err, blk < 0 ? PA_ERR_NEGATIVE_BLOCK : PA_ERR_OUT_OF_RANGE);
+    if (q.fresh == 0 || (!p.starts && q.n <= 0)) return q;
+    if (q.n < q.fresh) {
+        if (REPORT) set_error(p.d_err, PA_ERR_INVALID_ARG);
+        return q;
+    }
+    if (REPORT && (q.n > p.max_context || q.fresh > p.max_q)) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
+    if (!p.starts) {
+        q.units = 1;  // the siblings share it
+    } else {
+        const int64_t rows = (int64_t)min(q.fresh, p.max_q) * p.heads;
+        q.units = (int)((rows + p.unit_rows - 1) / p.unit_rows);
+    }
+    if (p.causal) {
+        const int64_t base = q.n - q.fresh;
+        q.first = (int)((base + 2 + (p.unit_rows - 1) / p.heads + kTok - 1) / kTok) + 1;
+        q.step = p.heads;
+    } else {
+        q.first = (min(q.n, p.max_context) + kTok - 1) / kTok;
+    }
+    return q;
+}
+
+// A stretch's share of one unit.
+struct Part {
+    int32_t seq;
+    int32_t row;          // first query row of the unit, over the whole call
+    int32_t rows;         // its rows
+    int32_t token;        // first row's index within the sequence's rows
+    int32_t limit;        // tokens that the unit's last row sees
+    int32_t t0, t1;       // tiles
+    int32_t tiles;        // of the whole unit
+    int64_t unit_at;      // the unit's place on the line
+    Seq q;
+};
+
+struct Line {
+    int64_t at, end;      // what is left of the stretch
+    int64_t seq_at;       // place of sequence s on the line
+    int32_t s;
+};
+
+// The next share of the stretch, skipping places that the line holds too many.
+PA_DEVICE bool next_part(const Params& p, Line& l, Part& w) {
+    while (l.at < l.end && l.s < p.seqs) {
+        const Seq q = read_seq<false>(p, l.s);
+        const int64_t all = q.before(q.units);
+        if (l.at >= l.seq_at + all) {
+            l.seq_at += all;
+            ++l.s;
             continue;
         }
-        const uint32_t* kr = (const uint32_t*)(
-            p.rows + ((int64_t)blk * p.block_size + j % p.block_size) * width);
-        float2 kf[kLatentPairs];
-        float d = 0.f;
-#pragma unroll
-        for (int c = 0; c < kLatentPairs; ++c) {
-            const int x = 2 * lane + 64 * c;
-            const uint32_t w = x < width ? kr[x >> 1] : 0;
-            kf[c] = make_float2(bf16_lo(w), bf16_hi(w));
-            d += qf[c].x * kf[c].x + qf[c].y * kf[c].y;
+        int64_t lo = 0, hi = q.units - 1;  // last unit that begins at or before `at`
+        const int64_t off = l.at - l.seq_at;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) >> 1;
+            if (q.before(mid) <= off) lo = mid; else hi = mid - 1;
         }
+        const int u = (int)lo;
+        const int64_t begin = l.seq_at + q.before(u), stop = l.seq_at + q.before(u + 1);
+        const int g = p.siblings > 1 ? (int)(blockIdx.x % p.siblings) : 0;
+        const int r0 = p.starts ? u * p.unit_rows : g * p.unit_rows;
+        const int all_rows = min(q.fresh, p.max_q) * p.heads;
+        const int rows = min(p.unit_rows, all_rows - r0);
+        int seen = q.n;
+        if (p.causal) seen = q.n - q.fresh + (r0 + rows - 1) / p.heads + 1;
+        seen = min(seen, p.max_context);
+        const int tiles = (seen + kTok - 1) / kTok;
+        const int t0 = (int)(l.at - begin);
+        const int t1 = (int)min((int64_t)tiles, l.end - begin);
+        l.at = min(stop, l.end);
+        if (t0 >= t1) continue;
+        w.seq = l.s;
+        w.row = q.start * p.heads + r0;
+        w.rows = rows;
+        w.token = r0;
+        w.limit = seen;
+        w.t0 = t0;
+        w.t1 = t1;
+        w.tiles = tiles;
+        w.unit_at = begin;
+        w.q = q;
+        return true;
+    }
+    return false;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_rows,
+              const Params p) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars* bars = reinterpret_cast<Bars*>(smem + p.off_bars);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pairs = p.latent_dim >> 7;
+    const int group = blockIdx.x / p.siblings;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_empty, 1);
+        mbar_init(&bars->o_free, 128);
+        for (int i = 0; i < kMaxPairs; ++i) {
+            mbar_init(&bars->pair_full[i], 1);
+            mbar_init(&bars->pair_empty[i], 1);
+        }
+        for (int i = 0; i < kMaxRope; ++i) {
+            mbar_init(&bars->rope_full[i], 1);
+            mbar_init(&bars->rope_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->s_full[i], 2);
+            mbar_init(&bars->p_full[i], 128);
+            mbar_init(&bars->pv_done[i], 1);
+        }
+        bars->abort = 0;
+        bars->seq = p.seqs;
+        bars->at = 0;
+        fence_mbar_init();
+        tc::prefetch_tmap(&tmap_q);
+        tc::prefetch_tmap(&tmap_rows);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&bars->tmem_base, 512);
+        tc::tmem_relinquish();
+    }
+    griddep_wait();
+    griddep_launch();
+
+    // the line's length, then the sequence in which this stretch begins: each
+    // thread adds up an equal run of sequences, and the one whose run holds the
+    // stretch's first tile walks it
+    const int run = (p.seqs + kThreads - 1) / kThreads;
+    const int s0 = min(p.seqs, (int)threadIdx.x * run), s1 = min(p.seqs, s0 + run);
+    int64_t mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        const Seq q = blockIdx.x == 0 ? read_seq<true>(p, s) : read_seq<false>(p, s);
+        mine += q.before(q.units);
+    }
+    int64_t upto = mine;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-        d *= p.scale_log2;
-        const float up = fmaxf(m, d);
-        const float f = m == -INFINITY ? 0.f : exp2f(m - up), w = exp2f(d - up);
-        m = up;
-        l = l * f + w;
-#pragma unroll
-        for (int c = 0; c < kLatentPairs; ++c) {
-            acc[c].x = acc[c].x * f + w * kf[c].x;
-            acc[c].y = acc[c].y * f + w * kf[c].y;
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += x;
+    }
+    if (lane == 31) bars->scan[warp] = upto;
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = bars->tmem_base;
+    int64_t total = 0, ahead = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) ahead += bars->scan[w];
+        total += bars->scan[w];
+    }
+    const int64_t per = max((total + p.groups - 1) / p.groups, (int64_t)p.min_tiles);
+    Line line;
+    line.at = min(total, group * per);
+    line.end = min(total, line.at + per);
+    ahead += upto - mine;
+    if (line.at < line.end && ahead <= line.at && line.at < ahead + mine) {
+        int64_t at = ahead;
+        for (int s = s0; s < s1; ++s) {
+            const Seq q = read_seq<false>(p, s);
+            const int64_t all = q.before(q.units);
+            if (line.at < at + all) {
+                bars->seq = s;
+                bars->at = at;
+                break;
+            }
+            at += all;
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint32_t* out = (uint32_t*)(p.out + row * p.latent_dim);
+    __syncthreads();
+    line.s = bars->seq;
+    line.seq_at = bars->at;
+    Part w;
+
+    const uint32_t tP = smem_u32(smem + p.off_p);
+    const uint32_t tRope = smem_u32(smem + p.off_rope);
+    const uint32_t tPairs = smem_u32(smem + p.off_pairs);
+    const int p_bytes = p.R * 128;
+    // S of tile i in columns [64 (i mod 2), + 64); O^T of pair m in [128 + m R, + R)
+    auto tS = [&](int64_t i) { return tmem + 64u * (uint32_t)(i & 1); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        const int bp = 1 << p.log2_bp;
+        const int box = min(bp, kTok);               // rows of one box
+        const int pages = kTok / box;                // boxes of one tile
+        bool ok = true;
+        uint32_t pair_n = 0, rope_n = 0, q_n = 0;    // loads issued so far
+        int64_t it = 0;
+        for (int unit = 0; ok && next_part(p, line, w); ++unit) {
+            const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
+            auto fetch = [&](int t) -> int32_t {     // this lane's page of tile t; -1 past the end
+                const int64_t pos = (int64_t)t * kTok + lane * box;
+                if (lane >= pages || t >= w.t1 || pos >= w.limit) return INT32_MIN;
+                const int64_t e = pos >> p.log2_bp;
+                return e < p.max_blocks ? max(__ldg(table + e), -1) : p.num_blocks;
+            };
+            int32_t next = fetch(w.t0);
+            for (int t = w.t0; t < w.t1; ++t, ++it) {
+                const int32_t id = next;
+                next = fetch(t + 1);
+                bool live = id != INT32_MIN;
+                if (live && (id < 0 || id >= p.num_blocks)) {
+                    set_error(p.d_err, id < 0 ? PA_ERR_NEGATIVE_BLOCK : PA_ERR_OUT_OF_RANGE);
+                    live = false;
+                }
+                const uint32_t mask = __ballot_sync(0xffffffffu, live);
+                const int row = live ? (id << p.log2_bp) + ((t * kTok + lane * box) & (bp - 1)) : 0;
+                const uint32_t bytes = __popc(mask) * box * 128;
+                for (int m = 0; m < pairs; ++m, ++pair_n) {
+                    const int slot = pair_n % p.pair_slots;
+                    if (pair_n >= (uint32_t)p.pair_slots &&
+                        !(ok = wait_warp(&bars->pair_empty[slot], (pair_n / p.pair_slots - 1) & 1, bars, p.d_err)))
+                        break;
+                    uint64_t* bar = &bars->pair_full[slot];
+                    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
+                    __syncwarp();
+                    if (live) {
+                        unsigned char* dst = smem + p.off_pairs + slot * kPair + lane * box * 128;
+                        tc::tma_load_2d(dst, &tmap_rows, m * 128, row, bar);
+                        tc::tma_load_2d(dst + kBlock, &tmap_rows, m * 128 + 64, row, bar);
+                    }
+                }
+                if (!ok) break;
+                const int slot = rope_n % p.rope_slots;
+                if (rope_n >= (uint32_t)p.rope_slots &&
+                    !(ok = wait_warp(&bars->rope_empty[slot], (rope_n / p.rope_slots - 1) & 1, bars, p.d_err)))
+                    break;
+                uint64_t* bar = &bars->rope_full[slot];
+                if (lane == 0) {
+                    bars->valid[it & 3] = mask;
+                    mbar_arrive_expect_tx(bar, bytes);
+                }
+                __syncwarp();
+                if (live)
+                    tc::tma_load_2d(smem + p.off_rope + slot * kBlock + lane * box * 128, &tmap_rows,
+                                    p.latent_dim, row, bar);
+                ++rope_n;
+                if (t == w.t0) {  // Q behind the unit's first tile: it waits for the unit before
+                    if (unit > 0 && !(ok = wait_warp(&bars->q_empty, (unit - 1) & 1, bars, p.d_err))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bars->q_full, (2 * pairs + 1) * p.R * 128);
+                        for (int b = 0; b <= 2 * pairs; ++b)
+                            tc::tma_load_2d(smem + b * p.R * 128, &tmap_q, b * 64, w.row, &bars->q_full);
+                    }
+                    __syncwarp();
+                    ++q_n;
+                }
+            }
+        }
+        __syncwarp();
+        if (!ok) {  // a wait ran out: no copy may still be on its way when the CTA ends
+            for (uint32_t n = pair_n - min(pair_n, (uint32_t)p.pair_slots); n < pair_n; ++n)
+                mbar_wait(&bars->pair_full[n % p.pair_slots], (n / p.pair_slots) & 1, p.d_err);
+            for (uint32_t n = rope_n - min(rope_n, (uint32_t)p.rope_slots); n < rope_n; ++n)
+                mbar_wait(&bars->rope_full[n % p.rope_slots], (n / p.rope_slots) & 1, p.d_err);
+            if (q_n > 0) mbar_wait(&bars->q_full, (q_n - 1) & 1, p.d_err);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t idesc_s = tc::idesc_bf16_f32(64, kTok, 0, 0);
+        const uint32_t idesc_o = tc::idesc_bf16_f32(128, p.R, 1, 0);
+        const uint64_t dq = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t dk = tc::smem_desc_sw128(tPairs, 16, 1024);
+        const uint64_t dr = tc::smem_desc_sw128(tRope, 16, 1024);
+        const uint64_t dv = tc::smem_desc_sw128(tPairs, kBlock, 1024);
+        const uint64_t dp = tc::smem_desc_sw128(tP, 16, 1024);
+        const uint64_t q_block = (uint64_t)(p.R * 128) >> 4;
+        const int rope_steps = p.rope_dim >> 4;
+        uint32_t qk_n = 0, rope_n = 0, pv_n = 0;
+        auto qk = [&](int64_t i, bool last) -> bool {
+            for (int m = 0; m < pairs; ++m, ++qk_n) {
+                const int slot = qk_n % p.pair_slots;
+                if (!wait_warp(&bars->pair_full[slot], (qk_n / p.pair_slots) & 1, bars, p.d_err)) return false;
+                tc::fence_after_sync();
+                const uint64_t b = dk + (uint64_t)((slot * kPair) >> 4);
+                const uint64_t a = dq + 2 * m * q_block;
 #pragma unroll
-    for (int c = 0; c < kLatentPairs; ++c) {
-        const int x = 2 * lane + 64 * c;
-        if (x < p.latent_dim) out[x >> 1] = pack_bf16(acc[c].x * inv, acc[c].y * inv);
+                for (int k = 0; k < 8; ++k)
+                    tc::mma_ss_warp(tS(i), a + (k >> 2) * q_block + ((k & 3) * 32 >> 4),
+                                    b + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), idesc_s, m + k > 0 ? 1u : 0u);
+            }
+            const int slot = rope_n % p.rope_slots;
+            if (!wait_warp(&bars->rope_full[slot], (rope_n / p.rope_slots) & 1, bars, p.d_err)) return false;
+            ++rope_n;
+            tc::fence_after_sync();
+            for (int k = 0; k < rope_steps; ++k)
+                tc::mma_ss_warp(tS(i), dq + 2 * pairs * q_block + k * 2,
+                                dr + (uint64_t)((slot * kBlock) >> 4) + k * 2, idesc_s, 1u);
+            tc::commit_warp(&bars->rope_empty[slot]);
+            if (last) tc::commit_warp(&bars->q_empty);
+            tc::commit_warp(&bars->s_full[i & 1]);
+            if (lane == 0) mbar_arrive(&bars->s_full[i & 1]);  // hands on valid[] too
+            return true;
+        };
+        int64_t it = 0;
+        bool ok = true;
+        for (int unit = 0; ok && next_part(p, line, w); ++unit) {
+            if (!(ok = wait_warp(&bars->q_full, unit & 1, bars, p.d_err))) break;
+            tc::fence_after_sync();
+            ok = qk(it, w.t0 + 1 == w.t1);
+            for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
+                if (t + 1 < w.t1 && !(ok = qk(it + 1, t + 2 == w.t1))) break;
+                if (t == w.t0 && unit > 0 &&
+                    !(ok = wait_warp(&bars->o_free, (unit - 1) & 1, bars, p.d_err)))
+                    break;
+                if (!(ok = wait_warp(&bars->p_full[it & 1], (it >> 1) & 1, bars, p.d_err))) break;
+                tc::fence_after_sync();
+                const uint64_t b = dp + (uint64_t)(((it & 1) * p_bytes) >> 4);
+                for (int m = 0; m < pairs; ++m, ++pv_n) {
+                    const int slot = pv_n % p.pair_slots;
+                    const uint64_t a = dv + (uint64_t)((slot * kPair) >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma_ss_warp(tmem + 128 + m * p.R, a + (k * 2048 >> 4), b + (k * 32 >> 4), idesc_o,
+                                        (t > w.t0 || k > 0) ? 1u : 0u);
+                    tc::commit_warp(&bars->pair_empty[slot]);
+                }
+                tc::commit_warp(&bars->pv_done[it & 1]);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int quarter = warp & 3;                  // TMEM lanes 32 quarter ..
+        const int tid = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const bool active = quarter * 16 < p.R;
+        const int r0 = quarter * 16 + (lane >> 2), r1 = r0 + 8;
+        const int log2_box = min(p.log2_bp, 6);
+        int64_t it = 0;
+        // every warp walks all tiles even after a wait ran out (named barriers have no
+        // limit, so none may stay away)
+        bool ok = true;
+        int32_t chain_rows = 0, chain_row = 0, chain = 0;
+        for (int unit = 0; next_part(p, line, w); ++unit) {
+            int lim0 = 0, lim1 = 0;                    // tokens that the two rows see
+            if (r0 < w.rows) lim0 = p.causal ? w.q.n - w.q.fresh + (w.token + r0) / p.heads + 1 : w.q.n;
+            if (r1 < w.rows) lim1 = p.causal ? w.q.n - w.q.fresh + (w.token + r1) / p.heads + 1 : w.q.n;
+            lim0 = min(lim0, p.max_context);
+            lim1 = min(lim1, p.max_context);
+            const int ctx = min(w.q.n, p.max_context);
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+            for (int t = w.t0; t < w.t1; ++t, ++it) {
+                const int b = (int)(it & 1);
+                ok &= wait_warp(&bars->s_full[b], (it >> 1) & 1, bars, p.d_err);
+                tc::fence_after_sync();
+                const int pos = t * kTok;
+                const int boxes = kTok >> log2_box;
+                const uint32_t valid = *(volatile uint32_t*)&bars->valid[it & 3];
+                const bool whole = valid == (0xffffffffu >> (32 - boxes)) && pos + kTok <= ctx;
+                uint32_t s[32];
+                float t0 = -INFINITY, t1 = -INFINITY;
+                bool grow = false;
+                if (active) {
+                    tmem_ld_16x256_x8(tS(it) + lanes, s);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        s[e] = __float_as_uint(__uint_as_float(s[e]) * p.scale_log2);
+                    if (!whole || pos + kTok > min(lim0, lim1)) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int c = (e >> 2) * 8 + (lane & 3) * 2 + (e & 1);
+                            const int lim = (e & 2) ? lim1 : lim0;
+                            if (pos + c >= lim || !((valid >> (c >> log2_box)) & 1)) s[e] = 0xff800000u;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        t0 = fmaxf(t0, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                        t1 = fmaxf(t1, fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
+                    }
+#pragma unroll
+                    for (int off = 1; off < 4; off <<= 1) {
+                        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, off));
+                        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, off));
+                    }
+                    if (m0 == -INFINITY) m0 = t0;
+                    if (m1 == -INFINITY) m1 = t1;
+                    grow = t0 > m0 + kRescale || t1 > m1 + kRescale;
+                }
+                if (t > w.t0 && named_any(1, grow)) {
+                    // O^T columns and l of the rows whose reference moves
+                    const float n0 = t0 > m0 + kRescale ? t0 : m0, n1 = t1 > m1 + kRescale ? t1 : m1;
+                    const float f0 = m0 == n0 ? 1.f : ex2(m0 - n0), f1 = m1 == n1 ? 1.f : ex2(m1 - n1);
+                    if (active && (lane & 3) == 0) {
+                        bars->factor[r0] = f0;
+                        bars->factor[r1] = f1;
+                    }
+                    if (active) {
+                        l0 *= f0;
+                        l1 *= f1;
+                        m0 = n0;
+                        m1 = n1;
+                    }
+                    ok &= wait_warp(&bars->pv_done[b ^ 1], ((it - 1) >> 1) & 1, bars, p.d_err);
+                    tc::fence_after_sync();
+                    named_sync(2);
+#pragma unroll 1
+                    for (int c = 0; c < pairs * p.R; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld_x16(tmem + 128 + c + lanes, o);
+                        tc::tmem_wait_ld();
+                        const int h = c % p.R;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * bars->factor[h + e]);
+                        tmem_st_x16(tmem + 128 + c + lanes, o);
+                    }
+                    tc::tmem_wait_st();
+                }
+                // P's buffer was last read by the product two tiles ago
+                if (it >= 2) ok &= wait_warp(&bars->pv_done[b], ((it >> 1) - 1) & 1, bars, p.d_err);
+                if (active) {
+                    const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+                    const uint32_t dst = tP + b * p_bytes;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float a0 = ex2(__uint_as_float(s[4 * i]) - u0);
+                        const float a1 = ex2(__uint_as_float(s[4 * i + 1]) - u0);
+                        const float c0 = ex2(__uint_as_float(s[4 * i + 2]) - u1);
+                        const float c1 = ex2(__uint_as_float(s[4 * i + 3]) - u1);
+                        // P as bf16 (the operand type of the tile that it multiplies); the
+                        // sums are of the rounded values, so the weights still add up to one
+                        const uint32_t a = pack_bf16(a0, a1), c = pack_bf16(c0, c1);
+                        l0 += bf16_lo(a) + bf16_hi(a);
+                        l1 += bf16_lo(c) + bf16_hi(c);
+                        const uint32_t col = (uint32_t)((i ^ (r0 & 7)) * 16 + (lane & 3) * 4);
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + r0 * 128 + col), "r"(a) : "memory");
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + r1 * 128 + col), "r"(c) : "memory");
+                    }
+                }
+                if (!whole) {
+                    // tokens that nobody wrote or loaded: their probability is zero, and
+                    // so must their value be (zero times NaN is NaN)
+                    const int tok = tid & 63;
+                    const int page_end = ((w.limit + (1 << log2_box) - 1) >> log2_box) << log2_box;
+                    if (pos + tok >= min(ctx, page_end) || !((valid >> (tok >> log2_box)) & 1)) {
+                        for (int m = tid >> 6; m < 2 * pairs; m += 2) {
+                            const uint32_t n = (uint32_t)(it * pairs + (m >> 1));
+                            const uint32_t at = tPairs + (n % p.pair_slots) * kPair + (m & 1) * kBlock + tok * 128;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
+                                             ::"r"(at + c * 16), "r"(0) : "memory");
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                tc::fence_before_sync();
+                mbar_arrive(&bars->p_full[b]);
+            }
+            // ---- the unit's end: O^T over l, or the part as it is
+            const bool cut = w.t0 > 0 || w.t1 < w.tiles;
+            // a stretch's first cut part in slot 0, its last in slot 1
+            const int which = w.t0 > 0 ? 0 : 1;
+            const int64_t slot = ((int64_t)group * 2 + which) * p.siblings + blockIdx.x % p.siblings;
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1) {
+                l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+                l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+            }
+            float* inv = bars->inv[unit & 1];
+            if (active && (lane & 3) == 0) {
+                inv[r0] = cut ? 1.f : l0 > 0.f ? 1.f / l0 : 0.f;
+                inv[r1] = cut ? 1.f : l1 > 0.f ? 1.f / l1 : 0.f;
+                if (cut) {
+                    p.stats[slot * p.R + r0] = make_float2(m0, l0);
+                    p.stats[slot * p.R + r1] = make_float2(m1, l1);
+                }
+            }
+            if (cut && w.t0 == 0) {  // this stretch holds the unit's beginning: it names the parts
+                chain = (int)((w.unit_at + w.tiles - 1) / per - group) + 1;
+                chain_row = w.row;
+                chain_rows = w.rows;
+            }
+            ok &= wait_warp(&bars->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, bars, p.d_err);
+            tc::fence_after_sync();
+            named_sync(2);
+            for (int m = 0; m < pairs; ++m) {
+                for (int c = 0; c < p.R; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld_x16(tmem + 128 + m * p.R + c + lanes, o);
+                    tc::tmem_wait_ld();
+                    if (cut) {
+                        float* dst = p.parts + (slot * p.R + c) * p.latent_dim + m * 128 + tid;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (c + e < w.rows) dst[(int64_t)e * p.latent_dim] = __uint_as_float(o[e]);
+                    } else {
+                        // neighbouring lanes swap rows, so that each stores two dims of one row
+                        const int odd = lane & 1;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float a = __uint_as_float(o[e]) * inv[c + e];
+                            const float d = __uint_as_float(o[e + 1]) * inv[c + e + 1];
+                            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : d, 1);
+                            const int row = c + e + odd;
+                            if (row < w.rows) {
+                                uint16_t* dst = p.out + (int64_t)(w.row + row) * p.latent_dim + m * 128 + (tid & ~1);
+                                *reinterpret_cast<uint32_t*>(dst) = odd ? pack_bf16(got, d) : pack_bf16(a, got);
+                            }
+                        }
+                    }
+                }
+            }
+            tc::fence_before_sync();
+            mbar_arrive(&bars->o_free);
+        }
+        if (tid == 0) p.meta[blockIdx.x] = make_int4(ok ? chain : 0, chain_row, chain_rows, 0);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
     }
 }
 
-static pa_status latent_attention(const pa_latent_pool* pool, const void* q, int32_t heads,
-                                  const int32_t* starts, const int32_t* tables,
-                                  int32_t max_blocks, const int32_t* lens, int32_t seqs,
-                                  int32_t max_q, int32_t total_q, int32_t max_context, float scale,
-                                  int causal,
-                                  void* out, int32_t* d_err, cudaStream_t stream) {
-    LatentParams p;
-    p.rows = (const uint16_t*)pool->rows;
+// Joins the parts of one cut unit: out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// Block (row, stretch in which the unit begins); part 0 is that stretch's last,
+// part i the first of the i-th stretch behind it.  A thread holds four dims and
+// every gridlike share of the parts; the shares meet in shared memory.
+__global__ void __launch_bounds__(512) latent_merge_kernel(const Params p) {
+    griddep_wait();
+    const int4 meta = p.meta[blockIdx.y];
+    if (meta.x < 2 || (int)blockIdx.x >= meta.z) return;
+    const int r = blockIdx.x;
+    const int group = blockIdx.y / p.siblings, sib = blockIdx.y % p.siblings;
+    const int columns = p.latent_dim >> 2;
+    const int col = threadIdx.x % columns, share = threadIdx.x / columns, shares = blockDim.x / columns;
+    auto slot = [&](int i) -> int64_t {
+        return (((int64_t)group + i) * 2 + (i == 0 ? 1 : 0)) * p.siblings + sib;
+    };
+    float top = -INFINITY;
+    for (int i = 0; i < meta.x; ++i) top = fmaxf(top, p.stats[slot(i) * p.R + r].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int i = share; i < meta.x; i += shares) {
+        const float2 st = p.stats[slot(i) * p.R + r];
+        const float4 o = reinterpret_cast<const float4*>(p.parts + (slot(i) * p.R + r) * p.latent_dim)[col];
+        const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
+        l += f * st.y;
+        acc.x += f * o.x;
+        acc.y += f * o.y;
+        acc.z += f * o.z;
+        acc.w += f * o.w;
+    }
+    __shared__ float4 sums[512];
+    __shared__ float ls[512];
+    sums[threadIdx.x] = acc;
+    ls[threadIdx.x] = l;
+    __syncthreads();
+    if (share > 0) return;
+    for (int i = 1; i < shares; ++i) {
+        const float4 o = sums[i * columns + col];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
+        l += ls[i * columns + col];
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint2* dst = reinterpret_cast<uint2*>(p.out + (int64_t)(meta.y + r) * p.latent_dim) + col;
+    *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+}
+
+// ---------------------------------------------------------------- host side
+// Shapes of a call: rows of a unit, siblings, stretches, shared memory.
+struct Shape {
+    int siblings, unit_rows, R, groups;
+    size_t meta_bytes, stats_bytes, bytes;
+};
+
+static size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+static Shape shape_of(const pa_latent_pool* pool, int heads, int seqs, bool prefill, int max_q,
+                      int total_q, int max_context) {
+    Shape s;
+    int64_t units;
+    if (max_q > total_q) max_q = total_q;
+    if (!prefill) {
+        s.siblings = (heads + 63) / 64;
+        s.unit_rows = (heads + s.siblings - 1) / s.siblings;
+        units = seqs;
+    } else {
+        s.siblings = 1;
+        const int64_t rows = (int64_t)max_q * heads;
+        s.unit_rows = (int)(rows < 64 ? rows : 64);
+        units = (int64_t)total_q * heads / s.unit_rows + seqs;  // a last one a sequence is not full
+    }
+    s.R = (s.unit_rows + 15) / 16 * 16;
+    const int64_t tiles = units * ((max_context + kTok - 1) / kTok + 2);
+    const int64_t most = device_sm_count() / s.siblings;
+    s.groups = (int)(tiles < most ? tiles : most);
+    if (s.groups < 1) s.groups = 1;
+    const size_t slots = (size_t)2 * s.groups * s.siblings;
+    s.meta_bytes = round256((size_t)s.groups * s.siblings * sizeof(int4));
+    s.stats_bytes = round256(slots * s.R * sizeof(float2));
+    s.bytes = s.meta_bytes + s.stats_bytes + slots * s.R * pool->latent_dim * sizeof(float);
+    return s;
+}
+
+static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t heads,
+                           const int32_t* starts, const int32_t* tables, int32_t max_blocks,
+                           const int32_t* lens, int32_t seqs, int32_t max_q, int32_t total_q,
+                           int32_t max_context, float scale, int causal, void* out, void* workspace,
+                           size_t workspace_bytes, int32_t* d_err, cudaStream_t stream) {
+    const Shape sh = shape_of(pool, heads, seqs, starts != nullptr, max_q, total_q, max_context);
+    if (workspace == nullptr || workspace_bytes < sh.bytes || !aligned16(workspace))
+        return PA_ERR_INVALID_ARG;
+    Params p;
     p.num_blocks = pool->num_blocks;
-    p.block_size = pool->block_size;
+    p.log2_bp = ilog2(pool->block_size);
     p.latent_dim = pool->latent_dim;
     p.rope_dim = pool->rope_dim;
-    p.q = (const uint16_t*)q;
     p.heads = heads;
     p.starts = starts;
     p.lens = lens;
@@ -118,15 +811,65 @@ static pa_status latent_attention(const pa_latent_pool* pool, const void* q, int
     p.max_context = max_context;
     p.causal = causal;
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.siblings = sh.siblings;
+    p.unit_rows = sh.unit_rows;
+    p.R = sh.R;
+    p.groups = sh.groups;
+    p.min_tiles = 2;
+    // shared memory: Q | P (two) | rotary ring | pair ring | barriers.  The S product
+    // reads 64 rows of Q whatever R is: for R < 64 it reads on into what follows, whose
+    // values reach only rows of S that nobody uses.
+    const int pairs = pool->latent_dim / 128;
+    p.off_p = (2 * pairs + 1) * sh.R * 128;
+    p.off_rope = p.off_p + 2 * sh.R * 128;
+    const int room = kSmemLimit - 1024 - kBarBytes - p.off_rope;
+    p.rope_slots = (room - 2 * kBlock) / kPair >= 2 * pairs ? 2 : 1;
+    p.off_pairs = p.off_rope + p.rope_slots * kBlock;
+    p.pair_slots = (room - p.rope_slots * kBlock) / kPair;
+    if (p.pair_slots > kMaxPairs) p.pair_slots = kMaxPairs;
+    p.off_bars = p.off_pairs + p.pair_slots * kPair;
+    const int smem = p.off_bars + kBarBytes + 1024;
     p.out = (uint16_t*)out;
+    p.meta = (int4*)workspace;
+    p.stats = (float2*)((char*)workspace + sh.meta_bytes);
+    p.parts = (float*)((char*)workspace + sh.meta_bytes + sh.stats_bytes);
     p.d_err = d_err;
-    const int64_t blocks = ((int64_t)max_q * heads + 3) / 4;
-    latent_rows_kernel<<<dim3((unsigned)blocks, (unsigned)seqs), 128, 0, stream>>>(p);
+
+    const uint64_t width = pool->latent_dim + pool->rope_dim;
+    CUtensorMap mq, mr;
+    const uint64_t qdims[2] = {width, (uint64_t)total_q * heads};
+    const uint64_t rdims[2] = {width, (uint64_t)pool->num_blocks * pool->block_size};
+    const uint64_t strides[1] = {width * 2};
+    const uint32_t qbox[2] = {64, (uint32_t)sh.R};
+    const uint32_t rbox[2] = {64, (uint32_t)(pool->block_size < kTok ? pool->block_size : kTok)};
+    if (!encode_bf16_map_sw128(&mq, q, 2, qdims, strides, qbox) ||
+        !encode_bf16_map_sw128(&mr, pool->rows, 2, rdims, strides, rbox))
+        return PA_ERR_CUDA;
+    static bool attr_done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= 64 || !attr_done[dev])) {
+        e = cudaFuncSetAttribute(latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        if (e == cudaSuccess && dev >= 0 && dev < 64) attr_done[dev] = true;
+    }
+    if (e == cudaSuccess)
+        e = launch_pdl(latent_kernel, dim3((unsigned)(sh.groups * sh.siblings)), dim3(kThreads), (size_t)smem,
+                       stream, mq, mr, p);
+    if (e == cudaSuccess && sh.groups > 1) {
+        // parts of one unit: about groups / sequences of them; many share a row's columns
+        const int columns = pool->latent_dim / 4;
+        const int shares = sh.groups >= 8 * seqs ? 512 / columns : 1;
+        e = launch_pdl(latent_merge_kernel, dim3((unsigned)sh.R, (unsigned)(sh.groups * sh.siblings)),
+                       dim3((unsigned)(columns * shares)), 0, stream, p);
+    }
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return PA_ERR_CUDA;
+    }
     return launch_status();
 }
 
-static pa_status check_latent_attention(const pa_latent_pool* pool, int32_t heads, int32_t seqs,
-                                        int32_t max_context) {
+static pa_status check(const pa_latent_pool* pool, int32_t heads, int32_t seqs, int32_t max_context) {
     pa_status st = check_latent_pool(pool);
     if (st != PA_OK) return st;
     if (heads <= 0 || seqs < 0 || max_context < 0) return PA_ERR_INVALID_ARG;
@@ -138,6 +881,7 @@ static pa_status check_latent_attention(const pa_latent_pool* pool, int32_t head
     return PA_OK;
 }
 
+}  // namespace lat
 }  // namespace pa
 
 using namespace pa;
@@ -146,9 +890,11 @@ extern "C" pa_status pa_decode_latent_workspace_bytes(const pa_latent_pool* pool
                                                       int32_t num_q_heads, int32_t max_context,
                                                       size_t* bytes) {
     if (bytes == nullptr) return PA_ERR_INVALID_ARG;
-    pa_status st = check_latent_attention(pool, num_q_heads, num_seqs, max_context);
+    pa_status st = lat::check(pool, num_q_heads, num_seqs, max_context);
     if (st != PA_OK) return st;
-    *bytes = 0;
+    *bytes = num_seqs == 0 || max_context == 0
+                 ? 0
+                 : lat::shape_of(pool, num_q_heads, num_seqs, false, 1, num_seqs, max_context).bytes;
     return PA_OK;
 }
 
@@ -157,17 +903,15 @@ extern "C" pa_status pa_decode_latent(const pa_latent_pool* pool, const void* q,
                                       const int32_t* context_lens, int32_t num_seqs,
                                       int32_t max_context, float scale, void* out, void* workspace,
                                       size_t workspace_bytes, int32_t* d_err, pa_stream_t stream) {
-    (void)workspace;
-    (void)workspace_bytes;
-    pa_status st = check_latent_attention(pool, num_q_heads, num_seqs, max_context);
+    pa_status st = lat::check(pool, num_q_heads, num_seqs, max_context);
     if (st != PA_OK) return st;
     if (max_blocks_per_seq < 0 || !(scale == scale)) return PA_ERR_INVALID_ARG;
     if (num_seqs == 0 || max_context == 0) return PA_OK;
     if (!q || !block_tables || !context_lens || !out) return PA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(pool->rows)) return PA_ERR_INVALID_ARG;
-    return latent_attention(pool, q, num_q_heads, nullptr, block_tables, max_blocks_per_seq,
-                            context_lens, num_seqs, 1, num_seqs, max_context, scale, 0, out, d_err,
-                            (cudaStream_t)stream);
+    return lat::attention(pool, q, num_q_heads, nullptr, block_tables, max_blocks_per_seq,
+                          context_lens, num_seqs, 1, num_seqs, max_context, scale, 0, out, workspace,
+                          workspace_bytes, d_err, (cudaStream_t)stream);
 }
 
 extern "C" pa_status pa_prefill_latent_workspace_bytes(const pa_latent_pool* pool, int32_t num_seqs,
@@ -175,9 +919,12 @@ extern "C" pa_status pa_prefill_latent_workspace_bytes(const pa_latent_pool* poo
                                                        int32_t max_q_len, int32_t max_context,
                                                        size_t* bytes) {
     if (bytes == nullptr || total_q < 0 || max_q_len < 0) return PA_ERR_INVALID_ARG;
-    pa_status st = check_latent_attention(pool, num_q_heads, num_seqs, max_context);
+    pa_status st = lat::check(pool, num_q_heads, num_seqs, max_context);
     if (st != PA_OK) return st;
-    *bytes = 0;
+    if ((int64_t)total_q * num_q_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    *bytes = num_seqs == 0 || total_q == 0 || max_q_len == 0 || max_context == 0
+                 ? 0
+                 : lat::shape_of(pool, num_q_heads, num_seqs, true, max_q_len, total_q, max_context).bytes;
     return PA_OK;
 }
 
@@ -188,9 +935,7 @@ extern "C" pa_status pa_prefill_latent(const pa_latent_pool* pool, const void* q
                                        int32_t max_q_len, int32_t max_context, float scale,
                                        int32_t causal, void* out, void* workspace,
                                        size_t workspace_bytes, int32_t* d_err, pa_stream_t stream) {
-    (void)workspace;
-    (void)workspace_bytes;
-    pa_status st = check_latent_attention(pool, num_q_heads, num_seqs, max_context);
+    pa_status st = lat::check(pool, num_q_heads, num_seqs, max_context);
     if (st != PA_OK) return st;
     if (total_q < 0 || max_q_len < 0 || max_blocks_per_seq < 0 || !(scale == scale))
         return PA_ERR_INVALID_ARG;
@@ -198,7 +943,8 @@ extern "C" pa_status pa_prefill_latent(const pa_latent_pool* pool, const void* q
     if (num_seqs == 0 || total_q == 0 || max_q_len == 0 || max_context == 0) return PA_OK;
     if (!q || !cu_seqlens_q || !context_lens || !block_tables || !out) return PA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(pool->rows)) return PA_ERR_INVALID_ARG;
-    return latent_attention(pool, q, num_q_heads, cu_seqlens_q, block_tables, max_blocks_per_seq,
-                            context_lens, num_seqs, max_q_len, total_q, max_context, scale,
-                            causal ? 1 : 0, out, d_err, (cudaStream_t)stream);
+    return lat::attention(pool, q, num_q_heads, cu_seqlens_q, block_tables, max_blocks_per_seq,
+                          context_lens, num_seqs, max_q_len < total_q ? max_q_len : total_q, total_q,
+                          max_context, scale, causal ? 1 : 0, out, workspace, workspace_bytes, d_err,
+                          (cudaStream_t)stream);
 }
