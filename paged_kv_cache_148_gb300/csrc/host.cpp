@@ -53,11 +53,11 @@ static bool encode_map_sw128(CUtensorMap* map, CUtensorMapDataType type, const v
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
     });
-    if (fn == nullptr || rank < 1 || rank > 3) return false;
-    cuuint64_t d[3];
-    cuuint64_t st[2];
-    cuuint32_t bx[3];
-    const cuuint32_t es[3] = {1, 1, 1};
+    if (fn == nullptr || rank < 1 || rank > 4) return false;
+    cuuint64_t d[4];
+    cuuint64_t st[3];
+    cuuint32_t bx[4];
+    const cuuint32_t es[4] = {1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) {
         d[i] = dims[i];
         bx[i] = box[i];

@@ -62,7 +62,7 @@ inline pa_status launch_status() {
 // Streaming multiprocessors of the current device (cached per device).
 int device_sm_count();
 
-// Tiled TMA descriptor of a bf16 tensor of rank 2 or 3 with the 128-byte
+// Tiled TMA descriptor of a bf16 tensor of rank 2 to 4 with the 128-byte
 // swizzle (dims innermost first, strides in bytes for dims 1.., box in
 // elements), encoded through the driver's cuTensorMapEncodeTiled.  false if
 // the driver entry point is missing or refuses the description.

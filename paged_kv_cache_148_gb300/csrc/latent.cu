@@ -15,12 +15,15 @@
 // columns and leave room for two S buffers, where O with rows as lanes would
 // fill all 512.
 //
-// Roles (192 threads, one CTA per SM):
+// Roles (224 threads, one CTA per SM):
 //   warp 0     TMA producer: Q of a unit; the tiles as boxes of one page x 64
 //              elements (128-byte swizzle) through the block table, into a
 //              ring of 128-dim pairs and a ring of rotary blocks.
-//   warp 1     MMA issuer: S of tile j + 1 before O^T of tile j, so that the
-//              softmax of one tile runs beside the products of others.
+//   warp 1     issues the MMAs of S, a pair as it lands.
+//   warp 6     issues the MMAs of O^T, a tile when its P is there.  Two issuers,
+//              each waiting for its own operands: with one, either product waits
+//              behind the other's (a tile's slots come free only behind its O^T,
+//              so the loads of S then take turns with the tensor core).
 //   warps 2-5  softmax of S (each warp 16 rows, a row over 4 lanes), base 2;
 //              P as bf16 into shared memory; the epilogue.
 //
@@ -46,13 +49,39 @@ namespace lat {
 
 constexpr int kTok = 64;             // tokens of a tile
 constexpr int kBlock = kTok * 128;   // bytes of 64 tokens x 64 elements
-constexpr int kPair = 2 * kBlock;
-constexpr int kThreads = 192;
-constexpr int kMaxPairs = 12;        // ring slots
-constexpr int kMaxRope = 3;
+constexpr int kThreads = 224;
 constexpr float kRescale = 16.0f;
 constexpr int kBarBytes = 1536;
 constexpr int kSmemLimit = 232448;   // 227 KB
+constexpr int kMaxParts = 12;        // ring slots
+constexpr int kMaxRope = 2;
+
+// Shared memory of a unit of up to R rows (a multiple of 16) and PAIRS x 128
+// latent dims: Q | P (two) | rotary ring | ring of parts | barriers.  A part is C
+// blocks of 64 dims of a tile, laid out [8 tokens][C][8 x 128 bytes]: one TMA box
+// of a page brings all C (a box costs the TMA unit about 50 cycles whatever its
+// size: a tile of 16-token pages took 2330 cycles with boxes of one block, 1000
+// with four), and both products find a stride for the 8-token groups in it.
+// The S product reads 64 rows of Q whatever R is: for R < 64 it reads on into what
+// follows, whose values reach only rows of S that nobody uses.  The ring holds two
+// tiles at least (S of the next tile goes before O^T of this one).
+template <int PAIRS, int R>
+struct Layout {
+    static constexpr int C = PAIRS % 2 == 0 ? 4 : 2;
+    static constexpr int kParts = 2 * PAIRS / C;             // of a tile
+    static constexpr int kPart = C * kBlock;
+    static constexpr int kP = (2 * PAIRS + 1) * R * 128;
+    static constexpr int kPBytes = R * 128;
+    static constexpr int kRope = kP + 2 * kPBytes;
+    static constexpr int kRoom = kSmemLimit - 1024 - kBarBytes - kRope;
+    static constexpr int kRopeSlots = (kRoom - 2 * kBlock) / kPart >= 2 * kParts ? 2 : 1;
+    static constexpr int kRing = kRope + kRopeSlots * kBlock;
+    static constexpr int kFit = (kRoom - kRopeSlots * kBlock) / kPart;
+    static constexpr int kSlots = kFit < kMaxParts ? kFit : kMaxParts;
+    static constexpr int kBars = kRing + kSlots * kPart;
+    static constexpr int kBytes = kBars + kBarBytes + 1024;
+    static_assert(kSlots >= 2 * kParts && kBytes <= kSmemLimit, "two tiles fit");
+};
 
 struct Params {
     int32_t num_blocks, log2_bp, latent_dim, rope_dim;
@@ -62,11 +91,9 @@ struct Params {
     float scale_log2;
     int32_t siblings;                // CTAs that share a unit's tiles (decode: 1 or 2)
     int32_t unit_rows;               // rows of a unit
-    int32_t R;                       // unit_rows rounded up to 16: N of the second product
+    int32_t R;                       // unit_rows rounded up to 16
     int32_t groups;                  // stretches
     int32_t min_tiles;               // least tiles a stretch
-    int32_t pair_slots, rope_slots;
-    int32_t off_p, off_rope, off_pairs, off_bars;  // shared memory
     uint16_t* out;
     int4* meta;                      // [groups * siblings]: parts of the unit cut behind this stretch
     float2* stats;                   // [2 * groups * siblings][R]: (max, sum) of a part's rows
@@ -76,7 +103,7 @@ struct Params {
 
 struct Bars {
     uint64_t q_full, q_empty, o_free;
-    uint64_t pair_full[kMaxPairs], pair_empty[kMaxPairs];
+    uint64_t part_full[kMaxParts], part_empty[kMaxParts];
     uint64_t rope_full[kMaxRope], rope_empty[kMaxRope];
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint32_t tmem_base;
@@ -265,24 +292,26 @@ PA_DEVICE bool next_part(const Params& p, Line& l, Part& w) {
     return false;
 }
 
+template <int PAIRS, int R>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_rows,
-              const Params p) {
+              const __grid_constant__ CUtensorMap tmap_rope, const Params p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Bars* bars = reinterpret_cast<Bars*>(smem + p.off_bars);
+    using L = Layout<PAIRS, R>;
+    Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pairs = p.latent_dim >> 7;
+    constexpr int kDim = PAIRS * 128;
     const int group = blockIdx.x / p.siblings;
 
     if (threadIdx.x == 0) {
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->o_free, 128);
-        for (int i = 0; i < kMaxPairs; ++i) {
-            mbar_init(&bars->pair_full[i], 1);
-            mbar_init(&bars->pair_empty[i], 1);
+        for (int i = 0; i < kMaxParts; ++i) {
+            mbar_init(&bars->part_full[i], 1);
+            mbar_init(&bars->part_empty[i], 1);
         }
         for (int i = 0; i < kMaxRope; ++i) {
             mbar_init(&bars->rope_full[i], 1);
@@ -299,6 +328,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         fence_mbar_init();
         tc::prefetch_tmap(&tmap_q);
         tc::prefetch_tmap(&tmap_rows);
+        tc::prefetch_tmap(&tmap_rope);
     }
     if (warp == 1) {
         tc::tmem_alloc(&bars->tmem_base, 512);
@@ -356,10 +386,8 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     line.seq_at = bars->at;
     Part w;
 
-    const uint32_t tP = smem_u32(smem + p.off_p);
-    const uint32_t tRope = smem_u32(smem + p.off_rope);
-    const uint32_t tPairs = smem_u32(smem + p.off_pairs);
-    const int p_bytes = p.R * 128;
+    const uint32_t tP = smem_u32(smem + L::kP);
+    const uint32_t tRing = smem_u32(smem + L::kRing);
     // S of tile i in columns [64 (i mod 2), + 64); O^T of pair m in [128 + m R, + R)
     auto tS = [&](int64_t i) { return tmem + 64u * (uint32_t)(i & 1); };
 
@@ -369,7 +397,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const int box = min(bp, kTok);               // rows of one box
         const int pages = kTok / box;                // boxes of one tile
         bool ok = true;
-        uint32_t pair_n = 0, rope_n = 0, q_n = 0;    // loads issued so far
+        uint32_t part_n = 0, rope_n = 0, q_n = 0;    // loads issued so far
         int64_t it = 0;
         for (int unit = 0; ok && next_part(p, line, w); ++unit) {
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
@@ -391,24 +419,22 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 const uint32_t mask = __ballot_sync(0xffffffffu, live);
                 const int row = live ? (id << p.log2_bp) + ((t * kTok + lane * box) & (bp - 1)) : 0;
                 const uint32_t bytes = __popc(mask) * box * 128;
-                for (int m = 0; m < pairs; ++m, ++pair_n) {
-                    const int slot = pair_n % p.pair_slots;
-                    if (pair_n >= (uint32_t)p.pair_slots &&
-                        !(ok = wait_warp(&bars->pair_empty[slot], (pair_n / p.pair_slots - 1) & 1, bars, p.d_err)))
+                for (int m = 0; m < L::kParts; ++m, ++part_n) {
+                    const int slot = part_n % L::kSlots;
+                    if (part_n >= (uint32_t)L::kSlots &&
+                        !(ok = wait_warp(&bars->part_empty[slot], (part_n / L::kSlots - 1) & 1, bars, p.d_err)))
                         break;
-                    uint64_t* bar = &bars->pair_full[slot];
-                    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
+                    uint64_t* bar = &bars->part_full[slot];
+                    if (lane == 0) mbar_arrive_expect_tx(bar, L::C * bytes);
                     __syncwarp();
-                    if (live) {
-                        unsigned char* dst = smem + p.off_pairs + slot * kPair + lane * box * 128;
-                        tc::tma_load_2d(dst, &tmap_rows, m * 128, row, bar);
-                        tc::tma_load_2d(dst + kBlock, &tmap_rows, m * 128 + 64, row, bar);
-                    }
+                    if (live)
+                        tc::tma_load_4d(smem + L::kRing + slot * L::kPart + lane * box * (L::C * 128), &tmap_rows,
+                                        0, 0, m * L::C, row >> 3, bar);
                 }
                 if (!ok) break;
-                const int slot = rope_n % p.rope_slots;
-                if (rope_n >= (uint32_t)p.rope_slots &&
-                    !(ok = wait_warp(&bars->rope_empty[slot], (rope_n / p.rope_slots - 1) & 1, bars, p.d_err)))
+                const int slot = rope_n % L::kRopeSlots;
+                if (rope_n >= (uint32_t)L::kRopeSlots &&
+                    !(ok = wait_warp(&bars->rope_empty[slot], (rope_n / L::kRopeSlots - 1) & 1, bars, p.d_err)))
                     break;
                 uint64_t* bar = &bars->rope_full[slot];
                 if (lane == 0) {
@@ -417,15 +443,15 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 }
                 __syncwarp();
                 if (live)
-                    tc::tma_load_2d(smem + p.off_rope + slot * kBlock + lane * box * 128, &tmap_rows,
-                                    p.latent_dim, row, bar);
+                    tc::tma_load_2d(smem + L::kRope + slot * kBlock + lane * box * 128, &tmap_rope,
+                                    kDim, row, bar);
                 ++rope_n;
                 if (t == w.t0) {  // Q behind the unit's first tile: it waits for the unit before
                     if (unit > 0 && !(ok = wait_warp(&bars->q_empty, (unit - 1) & 1, bars, p.d_err))) break;
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(&bars->q_full, (2 * pairs + 1) * p.R * 128);
-                        for (int b = 0; b <= 2 * pairs; ++b)
-                            tc::tma_load_2d(smem + b * p.R * 128, &tmap_q, b * 64, w.row, &bars->q_full);
+                        mbar_arrive_expect_tx(&bars->q_full, (2 * PAIRS + 1) * R * 128);
+                        for (int b = 0; b <= 2 * PAIRS; ++b)
+                            tc::tma_load_2d(smem + b * R * 128, &tmap_q, b * 64, w.row, &bars->q_full);
                     }
                     __syncwarp();
                     ++q_n;
@@ -434,71 +460,95 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         }
         __syncwarp();
         if (!ok) {  // a wait ran out: no copy may still be on its way when the CTA ends
-            for (uint32_t n = pair_n - min(pair_n, (uint32_t)p.pair_slots); n < pair_n; ++n)
-                mbar_wait(&bars->pair_full[n % p.pair_slots], (n / p.pair_slots) & 1, p.d_err);
-            for (uint32_t n = rope_n - min(rope_n, (uint32_t)p.rope_slots); n < rope_n; ++n)
-                mbar_wait(&bars->rope_full[n % p.rope_slots], (n / p.rope_slots) & 1, p.d_err);
+            for (uint32_t n = part_n - min(part_n, (uint32_t)L::kSlots); n < part_n; ++n)
+                mbar_wait(&bars->part_full[n % L::kSlots], (n / L::kSlots) & 1, p.d_err);
+            for (uint32_t n = rope_n - min(rope_n, (uint32_t)L::kRopeSlots); n < rope_n; ++n)
+                mbar_wait(&bars->rope_full[n % L::kRopeSlots], (n / L::kRopeSlots) & 1, p.d_err);
             if (q_n > 0) mbar_wait(&bars->q_full, (q_n - 1) & 1, p.d_err);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        const uint32_t idesc_s = tc::idesc_bf16_f32(64, kTok, 0, 0);
-        const uint32_t idesc_o = tc::idesc_bf16_f32(128, p.R, 1, 0);
+        // ------------------------------------------------------------ S
+        // An MMA's operands sit in warp-uniform registers.  Trip counts and branches
+        // come from votes, whose results the compiler knows to be uniform, and all
+        // offsets within a tile are constants: issue then keeps up with the tensor
+        // core (with descriptors from general registers each MMA took 100 cycles to
+        // issue, against 32 to 48 to run).
+        constexpr uint32_t idesc = tc::idesc_bf16_f32(64, kTok, 0, 0);
+        constexpr uint64_t q_block = (uint64_t)(R * 128) >> 4;
         const uint64_t dq = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
-        const uint64_t dk = tc::smem_desc_sw128(tPairs, 16, 1024);
-        const uint64_t dr = tc::smem_desc_sw128(tRope, 16, 1024);
-        const uint64_t dv = tc::smem_desc_sw128(tPairs, kBlock, 1024);
-        const uint64_t dp = tc::smem_desc_sw128(tP, 16, 1024);
-        const uint64_t q_block = (uint64_t)(p.R * 128) >> 4;
+        const uint64_t dk = tc::smem_desc_sw128(tRing, 16, L::C * 1024);
+        const uint64_t dr = tc::smem_desc_sw128(smem_u32(smem + L::kRope), 16, 1024);
         const int rope_steps = p.rope_dim >> 4;
-        uint32_t qk_n = 0, rope_n = 0, pv_n = 0;
-        auto qk = [&](int64_t i, bool last) -> bool {
-            for (int m = 0; m < pairs; ++m, ++qk_n) {
-                const int slot = qk_n % p.pair_slots;
-                if (!wait_warp(&bars->pair_full[slot], (qk_n / p.pair_slots) & 1, bars, p.d_err)) return false;
-                tc::fence_after_sync();
-                const uint64_t b = dk + (uint64_t)((slot * kPair) >> 4);
-                const uint64_t a = dq + 2 * m * q_block;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    tc::mma_ss_warp(tS(i), a + (k >> 2) * q_block + ((k & 3) * 32 >> 4),
-                                    b + (((k >> 2) * kBlock + (k & 3) * 32) >> 4), idesc_s, m + k > 0 ? 1u : 0u);
-            }
-            const int slot = rope_n % p.rope_slots;
-            if (!wait_warp(&bars->rope_full[slot], (rope_n / p.rope_slots) & 1, bars, p.d_err)) return false;
-            ++rope_n;
-            tc::fence_after_sync();
-            for (int k = 0; k < rope_steps; ++k)
-                tc::mma_ss_warp(tS(i), dq + 2 * pairs * q_block + k * 2,
-                                dr + (uint64_t)((slot * kBlock) >> 4) + k * 2, idesc_s, 1u);
-            tc::commit_warp(&bars->rope_empty[slot]);
-            if (last) tc::commit_warp(&bars->q_empty);
-            tc::commit_warp(&bars->s_full[i & 1]);
-            if (lane == 0) mbar_arrive(&bars->s_full[i & 1]);  // hands on valid[] too
-            return true;
-        };
-        int64_t it = 0;
+        uint32_t slot = 0, phase = 0, slot_r = 0, phase_r = 0, it = 0;
         bool ok = true;
-        for (int unit = 0; ok && next_part(p, line, w); ++unit) {
+        for (int unit = 0; ok && __any_sync(0xffffffffu, next_part(p, line, w)); ++unit) {
+            const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
             if (!(ok = wait_warp(&bars->q_full, unit & 1, bars, p.d_err))) break;
-            tc::fence_after_sync();
-            ok = qk(it, w.t0 + 1 == w.t1);
-            for (int t = w.t0; ok && t < w.t1; ++t, ++it) {
-                if (t + 1 < w.t1 && !(ok = qk(it + 1, t + 2 == w.t1))) break;
-                if (t == w.t0 && unit > 0 &&
-                    !(ok = wait_warp(&bars->o_free, (unit - 1) & 1, bars, p.d_err)))
-                    break;
+            for (int t = 0; t < n; ++t, ++it) {
+                // the softmax has read this buffer's last tile
+                if (it >= 2 && !(ok = wait_warp(&bars->p_full[it & 1], ((it >> 1) - 1) & 1, bars, p.d_err))) break;
+                const uint32_t d = tmem + 64u * (it & 1);
+#pragma unroll
+                for (int m = 0; m < L::kParts; ++m) {
+                    if (!(ok = wait_warp(&bars->part_full[slot], phase, bars, p.d_err))) break;
+                    tc::fence_after_sync();
+                    const uint64_t b = dk + (uint64_t)(slot * (L::kPart >> 4));
+                    const uint64_t a = dq + m * L::C * q_block;
+#pragma unroll
+                    for (int k = 0; k < 4 * L::C; ++k)
+                        tc::mma_ss_warp(d, a + (k >> 2) * q_block + ((k & 3) * 32 >> 4),
+                                        b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc, m + k > 0 ? 1u : 0u);
+                    if (++slot == L::kSlots) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok || !(ok = wait_warp(&bars->rope_full[slot_r], phase_r, bars, p.d_err))) break;
+                tc::fence_after_sync();
+                const uint64_t b = dr + (uint64_t)(slot_r * (kBlock >> 4));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < rope_steps)
+                        tc::mma_ss_warp(d, dq + 2 * PAIRS * q_block + k * 2, b + k * 2, idesc, 1u);
+                tc::commit_warp(&bars->rope_empty[slot_r]);
+                if (t + 1 == n) tc::commit_warp(&bars->q_empty);
+                tc::commit_warp(&bars->s_full[it & 1]);
+                if (lane == 0) mbar_arrive(&bars->s_full[it & 1]);  // hands on valid[] too
+                __syncwarp();
+                if (++slot_r == L::kRopeSlots) {
+                    slot_r = 0;
+                    phase_r ^= 1;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ------------------------------------------------------------ O^T
+        constexpr uint32_t idesc = tc::idesc_bf16_f32(128, R, 1, 0);
+        const uint64_t dv = tc::smem_desc_sw128(tRing, 1024, L::C * 1024);
+        const uint64_t dp = tc::smem_desc_sw128(tP, 16, 1024);
+        uint32_t slot = 0, it = 0;
+        bool ok = true;
+        for (int unit = 0; ok && __any_sync(0xffffffffu, next_part(p, line, w)); ++unit) {
+            const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
+            if (unit > 0 && !(ok = wait_warp(&bars->o_free, (unit - 1) & 1, bars, p.d_err))) break;
+            for (int t = 0; t < n; ++t, ++it) {
                 if (!(ok = wait_warp(&bars->p_full[it & 1], (it >> 1) & 1, bars, p.d_err))) break;
                 tc::fence_after_sync();
-                const uint64_t b = dp + (uint64_t)(((it & 1) * p_bytes) >> 4);
-                for (int m = 0; m < pairs; ++m, ++pv_n) {
-                    const int slot = pv_n % p.pair_slots;
-                    const uint64_t a = dv + (uint64_t)((slot * kPair) >> 4);
+                const uint64_t b = dp + (uint64_t)((it & 1) * (L::kPBytes >> 4));
+                const uint32_t first = t > 0 ? 1u : 0u;
+#pragma unroll
+                for (int m = 0; m < PAIRS; ++m) {
+                    constexpr int per = L::C / 2;            // pairs of a part
+                    const uint64_t a = dv + (uint64_t)(slot * (L::kPart >> 4) + m % per * (2048 >> 4));
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        tc::mma_ss_warp(tmem + 128 + m * p.R, a + (k * 2048 >> 4), b + (k * 32 >> 4), idesc_o,
-                                        (t > w.t0 || k > 0) ? 1u : 0u);
-                    tc::commit_warp(&bars->pair_empty[slot]);
+                        tc::mma_ss_warp(tmem + 128 + m * R, a + (k * 2 * L::C * 1024 >> 4), b + (k * 32 >> 4), idesc,
+                                        k > 0 ? 1u : first);
+                    if (m % per == per - 1) {
+                        tc::commit_warp(&bars->part_empty[slot]);
+                        if (++slot == L::kSlots) slot = 0;
+                    }
                 }
                 tc::commit_warp(&bars->pv_done[it & 1]);
             }
@@ -509,7 +559,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const int quarter = warp & 3;                  // TMEM lanes 32 quarter ..
         const int tid = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const bool active = quarter * 16 < p.R;
+        const bool active = quarter * 16 < R;
         const int r0 = quarter * 16 + (lane >> 2), r1 = r0 + 8;
         const int log2_box = min(p.log2_bp, 6);
         int64_t it = 0;
@@ -582,11 +632,11 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     tc::fence_after_sync();
                     named_sync(2);
 #pragma unroll 1
-                    for (int c = 0; c < pairs * p.R; c += 16) {
+                    for (int c = 0; c < PAIRS * R; c += 16) {
                         uint32_t o[16];
                         tmem_ld_x16(tmem + 128 + c + lanes, o);
                         tc::tmem_wait_ld();
-                        const int h = c % p.R;
+                        const int h = c % R;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * bars->factor[h + e]);
@@ -598,7 +648,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 if (it >= 2) ok &= wait_warp(&bars->pv_done[b], ((it >> 1) - 1) & 1, bars, p.d_err);
                 if (active) {
                     const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-                    const uint32_t dst = tP + b * p_bytes;
+                    const uint32_t dst = tP + b * L::kPBytes;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float a0 = ex2(__uint_as_float(s[4 * i]) - u0);
@@ -621,9 +671,10 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     const int tok = tid & 63;
                     const int page_end = ((w.limit + (1 << log2_box) - 1) >> log2_box) << log2_box;
                     if (pos + tok >= min(ctx, page_end) || !((valid >> (tok >> log2_box)) & 1)) {
-                        for (int m = tid >> 6; m < 2 * pairs; m += 2) {
-                            const uint32_t n = (uint32_t)(it * pairs + (m >> 1));
-                            const uint32_t at = tPairs + (n % p.pair_slots) * kPair + (m & 1) * kBlock + tok * 128;
+                        for (int m = tid >> 6; m < 2 * PAIRS; m += 2) {
+                            const uint32_t n = (uint32_t)(it * L::kParts + m / L::C);
+                            const uint32_t at = tRing + (n % L::kSlots) * L::kPart + (tok >> 3) * (L::C * 1024) +
+                                                m % L::C * 1024 + (tok & 7) * 128;
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
@@ -650,8 +701,8 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 inv[r0] = cut ? 1.f : l0 > 0.f ? 1.f / l0 : 0.f;
                 inv[r1] = cut ? 1.f : l1 > 0.f ? 1.f / l1 : 0.f;
                 if (cut) {
-                    p.stats[slot * p.R + r0] = make_float2(m0, l0);
-                    p.stats[slot * p.R + r1] = make_float2(m1, l1);
+                    p.stats[slot * R + r0] = make_float2(m0, l0);
+                    p.stats[slot * R + r1] = make_float2(m1, l1);
                 }
             }
             if (cut && w.t0 == 0) {  // this stretch holds the unit's beginning: it names the parts
@@ -662,16 +713,16 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             ok &= wait_warp(&bars->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, bars, p.d_err);
             tc::fence_after_sync();
             named_sync(2);
-            for (int m = 0; m < pairs; ++m) {
-                for (int c = 0; c < p.R; c += 16) {
+            for (int m = 0; m < PAIRS; ++m) {
+                for (int c = 0; c < R; c += 16) {
                     uint32_t o[16];
-                    tmem_ld_x16(tmem + 128 + m * p.R + c + lanes, o);
+                    tmem_ld_x16(tmem + 128 + m * R + c + lanes, o);
                     tc::tmem_wait_ld();
                     if (cut) {
-                        float* dst = p.parts + (slot * p.R + c) * p.latent_dim + m * 128 + tid;
+                        float* dst = p.parts + (slot * R + c) * kDim + m * 128 + tid;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (c + e < w.rows) dst[(int64_t)e * p.latent_dim] = __uint_as_float(o[e]);
+                            if (c + e < w.rows) dst[(int64_t)e * kDim] = __uint_as_float(o[e]);
                     } else {
                         // neighbouring lanes swap rows, so that each stores two dims of one row
                         const int odd = lane & 1;
@@ -682,7 +733,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                             const float got = __shfl_xor_sync(0xffffffffu, odd ? a : d, 1);
                             const int row = c + e + odd;
                             if (row < w.rows) {
-                                uint16_t* dst = p.out + (int64_t)(w.row + row) * p.latent_dim + m * 128 + (tid & ~1);
+                                uint16_t* dst = p.out + (int64_t)(w.row + row) * kDim + m * 128 + (tid & ~1);
                                 *reinterpret_cast<uint32_t*>(dst) = odd ? pack_bf16(got, d) : pack_bf16(a, got);
                             }
                         }
@@ -787,6 +838,33 @@ static Shape shape_of(const pa_latent_pool* pool, int heads, int seqs, bool pref
     return s;
 }
 
+template <int PAIRS, int R>
+static cudaError_t launch(const Params& p, const CUtensorMap& mq, const CUtensorMap& mr, const CUtensorMap& mp,
+                          cudaStream_t stream) {
+    constexpr int smem = Layout<PAIRS, R>::kBytes;
+    static bool attr_done[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev < 0 || dev >= 64 || !attr_done[dev])) {
+        e = cudaFuncSetAttribute(latent_kernel<PAIRS, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess && dev >= 0 && dev < 64) attr_done[dev] = true;
+    }
+    if (e != cudaSuccess) return e;
+    return launch_pdl(latent_kernel<PAIRS, R>, dim3((unsigned)(p.groups * p.siblings)), dim3(kThreads),
+                      (size_t)smem, stream, mq, mr, mp, p);
+}
+
+template <int R>
+static cudaError_t launch_rows(const Params& p, const CUtensorMap& mq, const CUtensorMap& mr,
+                               const CUtensorMap& mp, cudaStream_t stream) {
+    switch (p.latent_dim / 128) {
+        case 1: return launch<1, R>(p, mq, mr, mp, stream);
+        case 2: return launch<2, R>(p, mq, mr, mp, stream);
+        case 3: return launch<3, R>(p, mq, mr, mp, stream);
+        default: return launch<4, R>(p, mq, mr, mp, stream);
+    }
+}
+
 static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t heads,
                            const int32_t* starts, const int32_t* tables, int32_t max_blocks,
                            const int32_t* lens, int32_t seqs, int32_t max_q, int32_t total_q,
@@ -816,19 +894,6 @@ static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t he
     p.R = sh.R;
     p.groups = sh.groups;
     p.min_tiles = 2;
-    // shared memory: Q | P (two) | rotary ring | pair ring | barriers.  The S product
-    // reads 64 rows of Q whatever R is: for R < 64 it reads on into what follows, whose
-    // values reach only rows of S that nobody uses.
-    const int pairs = pool->latent_dim / 128;
-    p.off_p = (2 * pairs + 1) * sh.R * 128;
-    p.off_rope = p.off_p + 2 * sh.R * 128;
-    const int room = kSmemLimit - 1024 - kBarBytes - p.off_rope;
-    p.rope_slots = (room - 2 * kBlock) / kPair >= 2 * pairs ? 2 : 1;
-    p.off_pairs = p.off_rope + p.rope_slots * kBlock;
-    p.pair_slots = (room - p.rope_slots * kBlock) / kPair;
-    if (p.pair_slots > kMaxPairs) p.pair_slots = kMaxPairs;
-    p.off_bars = p.off_pairs + p.pair_slots * kPair;
-    const int smem = p.off_bars + kBarBytes + 1024;
     p.out = (uint16_t*)out;
     p.meta = (int4*)workspace;
     p.stats = (float2*)((char*)workspace + sh.meta_bytes);
@@ -836,25 +901,29 @@ static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t he
     p.d_err = d_err;
 
     const uint64_t width = pool->latent_dim + pool->rope_dim;
-    CUtensorMap mq, mr;
+    CUtensorMap mq, mr, mp;
     const uint64_t qdims[2] = {width, (uint64_t)total_q * heads};
-    const uint64_t rdims[2] = {width, (uint64_t)pool->num_blocks * pool->block_size};
     const uint64_t strides[1] = {width * 2};
     const uint32_t qbox[2] = {64, (uint32_t)sh.R};
-    const uint32_t rbox[2] = {64, (uint32_t)(pool->block_size < kTok ? pool->block_size : kTok)};
+    // the pool as [rows / 8][blocks of 64 dims][8][64], and as rows for the rotary part
+    const uint64_t rows = (uint64_t)pool->num_blocks * pool->block_size;
+    const uint32_t box = pool->block_size < kTok ? pool->block_size : kTok;
+    const uint64_t rdims[4] = {64, 8, (uint64_t)pool->latent_dim / 64, rows / 8};
+    const uint64_t rstrides[3] = {width * 2, 128, width * 16};
+    const uint32_t rbox[4] = {64, 8, pool->latent_dim % 256 == 0 ? 4u : 2u, box / 8};
+    const uint64_t pdims[2] = {width, rows};
+    const uint32_t pbox[2] = {64, box};
     if (!encode_bf16_map_sw128(&mq, q, 2, qdims, strides, qbox) ||
-        !encode_bf16_map_sw128(&mr, pool->rows, 2, rdims, strides, rbox))
+        !encode_bf16_map_sw128(&mr, pool->rows, 4, rdims, rstrides, rbox) ||
+        !encode_bf16_map_sw128(&mp, pool->rows, 2, pdims, strides, pbox))
         return PA_ERR_CUDA;
-    static bool attr_done[64] = {false};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev < 0 || dev >= 64 || !attr_done[dev])) {
-        e = cudaFuncSetAttribute(latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-        if (e == cudaSuccess && dev >= 0 && dev < 64) attr_done[dev] = true;
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (sh.R / 16) {
+        case 1: e = launch_rows<16>(p, mq, mr, mp, stream); break;
+        case 2: e = launch_rows<32>(p, mq, mr, mp, stream); break;
+        case 3: e = launch_rows<48>(p, mq, mr, mp, stream); break;
+        case 4: e = launch_rows<64>(p, mq, mr, mp, stream); break;
     }
-    if (e == cudaSuccess)
-        e = launch_pdl(latent_kernel, dim3((unsigned)(sh.groups * sh.siblings)), dim3(kThreads), (size_t)smem,
-                       stream, mq, mr, p);
     if (e == cudaSuccess && sh.groups > 1) {
         // parts of one unit: about groups / sequences of them; many share a row's columns
         const int columns = pool->latent_dim / 4;
