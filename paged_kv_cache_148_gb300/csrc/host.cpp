@@ -53,11 +53,11 @@ static bool encode_map_sw128(CUtensorMap* map, CUtensorMapDataType type, const v
             q == cudaDriverEntryPointSuccess)
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
     });
-    if (fn == nullptr || rank < 1 || rank > 4) return false;
-    cuuint64_t d[4];
-    cuuint64_t st[3];
-    cuuint32_t bx[4];
-    const cuuint32_t es[4] = {1, 1, 1, 1};
+    if (fn == nullptr || rank < 1 || rank > 5) return false;
+    cuuint64_t d[5];
+    cuuint64_t st[4];
+    cuuint32_t bx[5];
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) {
         d[i] = dims[i];
         bx[i] = box[i];

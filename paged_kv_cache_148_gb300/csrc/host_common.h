@@ -62,7 +62,7 @@ inline pa_status launch_status() {
 // Streaming multiprocessors of the current device (cached per device).
 int device_sm_count();
 
-// Tiled TMA descriptor of a bf16 tensor of rank 2 to 4 with the 128-byte
+// Tiled TMA descriptor of a bf16 tensor of rank 2 to 5 with the 128-byte
 // swizzle (dims innermost first, strides in bytes for dims 1.., box in
 // elements), encoded through the driver's cuTensorMapEncodeTiled.  false if
 // the driver entry point is missing or refuses the description.
@@ -73,21 +73,32 @@ bool encode_u8_map_sw128(CUtensorMap* map, const void* base, int rank, const uin
                          const uint64_t* strides, const uint32_t* box);
 
 // Launch with programmatic stream serialization (the kernel must call
-// griddep_wait() before touching memory its predecessor may write).
+// griddep_wait() before touching memory its predecessor may write), in clusters
+// of `cluster` blocks.
 template <typename Kern, typename... Args>
-inline cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                              Args... args) {
+inline cudaError_t launch_pdl_cluster(Kern kern, unsigned cluster, dim3 grid, dim3 block, size_t smem,
+                                      cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename Kern, typename... Args>
+inline cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                              Args... args) {
+    return launch_pdl_cluster(kern, 1, grid, block, smem, stream, args...);
 }
 
 }  // namespace pa

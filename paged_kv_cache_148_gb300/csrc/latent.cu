@@ -27,9 +27,7 @@
 //   warps 2-5  softmax of S (each warp 16 rows, a row over 4 lanes), base 2;
 //              P as bf16 into shared memory; the epilogue.
 //
-// All units' tiles of a call form one line, cut into equal stretches, one a CTA
-// (a CTA group of 2 for 65 to 128 heads of a decode: the siblings take half of
-// the heads each and stream the same tiles, so that one of them hits in L2).
+// All units' tiles of a call form one line, cut into equal stretches, one a CTA.
 // A unit whose tiles lie in one stretch is written at once; the parts of a cut
 // one go to the workspace as (max, sum, unnormalised O) in float32, and a second
 // kernel joins them.
@@ -37,22 +35,13 @@
 // The running reference of a row's scores moves only when its maximum grew by
 // more than 2^16 (bf16 has float32's range, so P loses nothing by it): the
 // rescaling of O^T, which takes all four warps, is then rare.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "host_common.h"
-#include "rope.cuh"
-#include "tcgen05.cuh"
+#include "latent.cuh"
 
 namespace pa {
 namespace lat {
 
-constexpr int kTok = 64;             // tokens of a tile
-constexpr int kBlock = kTok * 128;   // bytes of 64 tokens x 64 elements
 constexpr int kThreads = 224;
-constexpr float kRescale = 16.0f;
 constexpr int kBarBytes = 1536;
-constexpr int kSmemLimit = 232448;   // 227 KB
 constexpr int kMaxParts = 12;        // ring slots
 constexpr int kMaxRope = 2;
 
@@ -83,24 +72,6 @@ struct Layout {
     static_assert(kSlots >= 2 * kParts && kBytes <= kSmemLimit, "two tiles fit");
 };
 
-struct Params {
-    int32_t num_blocks, log2_bp, latent_dim, rope_dim;
-    int32_t heads;
-    const int32_t *starts, *lens, *tables;  // starts: null for one query a sequence
-    int32_t max_blocks, seqs, max_q, total_q, max_context, causal;
-    float scale_log2;
-    int32_t siblings;                // CTAs that share a unit's tiles (decode: 1 or 2)
-    int32_t unit_rows;               // rows of a unit
-    int32_t R;                       // unit_rows rounded up to 16
-    int32_t groups;                  // stretches
-    int32_t min_tiles;               // least tiles a stretch
-    uint16_t* out;
-    int4* meta;                      // [groups * siblings]: parts of the unit cut behind this stretch
-    float2* stats;                   // [2 * groups * siblings][R]: (max, sum) of a part's rows
-    float* parts;                    // [2 * groups * siblings][R][latent_dim]
-    int32_t* d_err;
-};
-
 struct Bars {
     uint64_t q_full, q_empty, o_free;
     uint64_t part_full[kMaxParts], part_empty[kMaxParts];
@@ -111,39 +82,9 @@ struct Bars {
     uint32_t valid[4];               // pages of a tile that were loaded, by tile mod 4
     float factor[64];                // rescaling factors of the rows
     float inv[2][64];                // one over the rows' sums, by unit mod 2
-    int64_t scan[8];
-    int64_t at, per;
-    int32_t seq;
+    Scan scan;
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier area");
-
-// A warp's bounded wait.  Once one has run out the CTA winds down: every later
-// wait that would block returns at once.
-PA_DEVICE bool wait_warp(uint64_t* bar, uint32_t parity, Bars* b, int32_t* d_err) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        const uint64_t t0 = global_timer_ns();
-        while (!(ok = mbar_try_wait(bar, parity))) {
-            if (*(volatile int32_t*)&b->abort) break;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-                set_error(d_err, PA_ERR_TIMEOUT);
-                *(volatile int32_t*)&b->abort = 1;
-                break;
-            }
-        }
-    }
-    return __all_sync(0xffffffffu, ok);
-}
-
-PA_DEVICE void named_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
-PA_DEVICE bool named_any(int id, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-        "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"(id), "r"((uint32_t)x) : "memory");
-    return r != 0;
-}
 
 // 16 lanes x 64 columns: thread t gets, for column group i of 8, rows t / 4 (regs
 // 4i, 4i + 1) and t / 4 + 8 (4i + 2, 4i + 3), columns 8i + 2 (t % 4) and the next.
@@ -179,119 +120,6 @@ PA_DEVICE void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
         : "memory");
 }
 
-// ---------------------------------------------------------------- the line of tiles
-// A sequence's units and the tiles that the line holds for each.  With a causal
-// mask unit u needs ceil(seen / 64) tiles, seen growing with u; the line gives it
-// first + u / heads, at least as many (at most two more) and with a sum in
-// closed form, so that a stretch finds its place without walking the units.
-struct Seq {
-    int32_t start, fresh, n;   // first query token; query tokens; context
-    int32_t units, first, step;  // tiles of unit u: first + u / step (step 0: first)
-
-    PA_DEVICE int64_t before(int64_t u) const {
-        if (step == 0) return u * first;
-        const int64_t k = u / step;
-        return u * first + step * (k * (k - 1) / 2) + k * (u - k * step);
-    }
-};
-
-template <bool REPORT>
-PA_DEVICE Seq read_seq(const Params& p, int s) {
-    Seq q;
-    q.units = q.first = q.step = 0;
-    q.start = p.starts ? __ldg(p.starts + s) : s;
-    q.fresh = p.starts ? __ldg(p.starts + s + 1) - q.start : 1;
-    q.n = __ldg(p.lens + s);
-    if (p.starts && (q.start < 0 || q.fresh < 0 || q.fresh > p.total_q - q.start)) {
-        if (REPORT) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
-        return q;
-    }
-    if (q.fresh == 0 || (!p.starts && q.n <= 0)) return q;
-    if (q.n < q.fresh) {
-        if (REPORT) set_error(p.d_err, PA_ERR_INVALID_ARG);
-        return q;
-    }
-    if (REPORT && (q.n > p.max_context || q.fresh > p.max_q)) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
-    if (!p.starts) {
-        q.units = 1;  // the siblings share it
-    } else {
-        const int64_t rows = (int64_t)min(q.fresh, p.max_q) * p.heads;
-        q.units = (int)((rows + p.unit_rows - 1) / p.unit_rows);
-    }
-    if (p.causal) {
-        const int64_t base = q.n - q.fresh;
-        q.first = (int)((base + 2 + (p.unit_rows - 1) / p.heads + kTok - 1) / kTok) + 1;
-        q.step = p.heads;
-    } else {
-        q.first = (min(q.n, p.max_context) + kTok - 1) / kTok;
-    }
-    return q;
-}
-
-// A stretch's share of one unit.
-struct Part {
-    int32_t seq;
-    int32_t row;          // first query row of the unit, over the whole call
-    int32_t rows;         // its rows
-    int32_t token;        // first row's index within the sequence's rows
-    int32_t limit;        // tokens that the unit's last row sees
-    int32_t t0, t1;       // tiles
-    int32_t tiles;        // of the whole unit
-    int64_t unit_at;      // the unit's place on the line
-    Seq q;
-};
-
-struct Line {
-    int64_t at, end;      // what is left of the stretch
-    int64_t seq_at;       // place of sequence s on the line
-    int32_t s;
-};
-
-// The next share of the stretch, skipping places that the line holds too many.
-PA_DEVICE bool next_part(const Params& p, Line& l, Part& w) {
-    while (l.at < l.end && l.s < p.seqs) {
-        const Seq q = read_seq<false>(p, l.s);
-        const int64_t all = q.before(q.units);
-        if (l.at >= l.seq_at + all) {
-            l.seq_at += all;
-            ++l.s;
-            continue;
-        }
-        int64_t lo = 0, hi = q.units - 1;  // last unit that begins at or before `at`
-        const int64_t off = l.at - l.seq_at;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) >> 1;
-            if (q.before(mid) <= off) lo = mid; else hi = mid - 1;
-        }
-        const int u = (int)lo;
-        const int64_t begin = l.seq_at + q.before(u), stop = l.seq_at + q.before(u + 1);
-        const int g = p.siblings > 1 ? (int)(blockIdx.x % p.siblings) : 0;
-        const int r0 = p.starts ? u * p.unit_rows : g * p.unit_rows;
-        const int all_rows = min(q.fresh, p.max_q) * p.heads;
-        const int rows = min(p.unit_rows, all_rows - r0);
-        int seen = q.n;
-        if (p.causal) seen = q.n - q.fresh + (r0 + rows - 1) / p.heads + 1;
-        seen = min(seen, p.max_context);
-        const int tiles = (seen + kTok - 1) / kTok;
-        const int t0 = (int)(l.at - begin);
-        const int t1 = (int)min((int64_t)tiles, l.end - begin);
-        l.at = min(stop, l.end);
-        if (t0 >= t1) continue;
-        w.seq = l.s;
-        w.row = q.start * p.heads + r0;
-        w.rows = rows;
-        w.token = r0;
-        w.limit = seen;
-        w.t0 = t0;
-        w.t1 = t1;
-        w.tiles = tiles;
-        w.unit_at = begin;
-        w.q = q;
-        return true;
-    }
-    return false;
-}
-
 template <int PAIRS, int R>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_rows,
@@ -303,7 +131,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kDim = PAIRS * 128;
-    const int group = blockIdx.x / p.siblings;
+    const int group = blockIdx.x;
 
     if (threadIdx.x == 0) {
         mbar_init(&bars->q_full, 1);
@@ -323,8 +151,6 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             mbar_init(&bars->pv_done[i], 1);
         }
         bars->abort = 0;
-        bars->seq = p.seqs;
-        bars->at = 0;
         fence_mbar_init();
         tc::prefetch_tmap(&tmap_q);
         tc::prefetch_tmap(&tmap_rows);
@@ -337,53 +163,12 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     griddep_wait();
     griddep_launch();
 
-    // the line's length, then the sequence in which this stretch begins: each
-    // thread adds up an equal run of sequences, and the one whose run holds the
-    // stretch's first tile walks it
-    const int run = (p.seqs + kThreads - 1) / kThreads;
-    const int s0 = min(p.seqs, (int)threadIdx.x * run), s1 = min(p.seqs, s0 + run);
-    int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) {
-        const Seq q = blockIdx.x == 0 ? read_seq<true>(p, s) : read_seq<false>(p, s);
-        mine += q.before(q.units);
-    }
-    int64_t upto = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += x;
-    }
-    if (lane == 31) bars->scan[warp] = upto;
+    int64_t per;
+    Line line = find_stretch<kThreads>(p, group, blockIdx.x == 0, bars->scan, per);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = bars->tmem_base;
-    int64_t total = 0, ahead = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) ahead += bars->scan[w];
-        total += bars->scan[w];
-    }
-    const int64_t per = max((total + p.groups - 1) / p.groups, (int64_t)p.min_tiles);
-    Line line;
-    line.at = min(total, group * per);
-    line.end = min(total, line.at + per);
-    ahead += upto - mine;
-    if (line.at < line.end && ahead <= line.at && line.at < ahead + mine) {
-        int64_t at = ahead;
-        for (int s = s0; s < s1; ++s) {
-            const Seq q = read_seq<false>(p, s);
-            const int64_t all = q.before(q.units);
-            if (line.at < at + all) {
-                bars->seq = s;
-                bars->at = at;
-                break;
-            }
-            at += all;
-        }
-    }
-    __syncthreads();
-    line.s = bars->seq;
-    line.seq_at = bars->at;
     Part w;
 
     const uint32_t tP = smem_u32(smem + L::kP);
@@ -690,7 +475,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             const bool cut = w.t0 > 0 || w.t1 < w.tiles;
             // a stretch's first cut part in slot 0, its last in slot 1
             const int which = w.t0 > 0 ? 0 : 1;
-            const int64_t slot = ((int64_t)group * 2 + which) * p.siblings + blockIdx.x % p.siblings;
+            const int64_t slot = (int64_t)group * 2 + which;
 #pragma unroll
             for (int off = 1; off < 4; off <<= 1) {
                 l0 += __shfl_xor_sync(0xffffffffu, l0, off);
@@ -762,11 +547,11 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const Params p) {
     const int4 meta = p.meta[blockIdx.y];
     if (meta.x < 2 || (int)blockIdx.x >= meta.z) return;
     const int r = blockIdx.x;
-    const int group = blockIdx.y / p.siblings, sib = blockIdx.y % p.siblings;
+    const int group = blockIdx.y;
     const int columns = p.latent_dim >> 2;
     const int col = threadIdx.x % columns, share = threadIdx.x / columns, shares = blockDim.x / columns;
     auto slot = [&](int i) -> int64_t {
-        return (((int64_t)group + i) * 2 + (i == 0 ? 1 : 0)) * p.siblings + sib;
+        return ((int64_t)group + i) * 2 + (i == 0 ? 1 : 0);
     };
     float top = -INFINITY;
     for (int i = 0; i < meta.x; ++i) top = fmaxf(top, p.stats[slot(i) * p.R + r].x);
@@ -803,36 +588,36 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const Params p) {
 }
 
 // ---------------------------------------------------------------- host side
-// Shapes of a call: rows of a unit, siblings, stretches, shared memory.
+// Shapes of a call: which kernel, rows of a unit, stretches, workspace.
 struct Shape {
-    int siblings, unit_rows, R, groups;
+    bool pair;
+    int unit_rows, R, groups;
     size_t meta_bytes, stats_bytes, bytes;
 };
 
 static size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
-static Shape shape_of(const pa_latent_pool* pool, int heads, int seqs, bool prefill, int max_q,
-                      int total_q, int max_context) {
+static Shape shape_of(const pa_latent_pool* pool, int heads, int seqs, int max_q, int total_q,
+                      int max_context) {
     Shape s;
-    int64_t units;
     if (max_q > total_q) max_q = total_q;
-    if (!prefill) {
-        s.siblings = (heads + 63) / 64;
-        s.unit_rows = (heads + s.siblings - 1) / s.siblings;
-        units = seqs;
+    const int64_t rows = (int64_t)max_q * heads;   // most of a sequence
+    s.pair = rows > 64 && pool->rope_dim == 64 && pool->latent_dim % 256 == 0;
+    if (s.pair) {
+        s.unit_rows = s.R = 128;
     } else {
-        s.siblings = 1;
-        const int64_t rows = (int64_t)max_q * heads;
-        s.unit_rows = (int)(rows < 64 ? rows : 64);
-        units = (int64_t)total_q * heads / s.unit_rows + seqs;  // a last one a sequence is not full
+        const int64_t units = (rows + 63) / 64;    // as even as two rows of units can be
+        s.unit_rows = units == 2 && max_q == 1 ? (int)((rows + 1) / 2) : (int)(rows < 64 ? rows : 64);
+        s.R = (s.unit_rows + 15) / 16 * 16;
     }
-    s.R = (s.unit_rows + 15) / 16 * 16;
+    // a sequence's last unit may not be full, and the line holds up to two tiles more a unit
+    const int64_t units = (int64_t)total_q * heads / s.unit_rows + seqs;
     const int64_t tiles = units * ((max_context + kTok - 1) / kTok + 2);
-    const int64_t most = device_sm_count() / s.siblings;
+    const int64_t most = device_sm_count() / (s.pair ? 2 : 1);
     s.groups = (int)(tiles < most ? tiles : most);
     if (s.groups < 1) s.groups = 1;
-    const size_t slots = (size_t)2 * s.groups * s.siblings;
-    s.meta_bytes = round256((size_t)s.groups * s.siblings * sizeof(int4));
+    const size_t slots = (size_t)2 * s.groups;
+    s.meta_bytes = round256((size_t)s.groups * sizeof(int4));
     s.stats_bytes = round256(slots * s.R * sizeof(float2));
     s.bytes = s.meta_bytes + s.stats_bytes + slots * s.R * pool->latent_dim * sizeof(float);
     return s;
@@ -850,7 +635,7 @@ static cudaError_t launch(const Params& p, const CUtensorMap& mq, const CUtensor
         if (e == cudaSuccess && dev >= 0 && dev < 64) attr_done[dev] = true;
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(latent_kernel<PAIRS, R>, dim3((unsigned)(p.groups * p.siblings)), dim3(kThreads),
+    return launch_pdl(latent_kernel<PAIRS, R>, dim3((unsigned)p.groups), dim3(kThreads),
                       (size_t)smem, stream, mq, mr, mp, p);
 }
 
@@ -865,12 +650,39 @@ static cudaError_t launch_rows(const Params& p, const CUtensorMap& mq, const CUt
     }
 }
 
+static cudaError_t launch_one(const Params& p, const void* q, const pa_latent_pool* pool, int64_t q_rows,
+                              cudaStream_t stream) {
+    const uint64_t width = pool->latent_dim + pool->rope_dim;
+    CUtensorMap mq, mr, mp;
+    const uint64_t qdims[2] = {width, (uint64_t)q_rows};
+    const uint64_t strides[1] = {width * 2};
+    const uint32_t qbox[2] = {64, (uint32_t)p.R};
+    // the pool as [rows / 8][blocks of 64 dims][8][64], and as rows for the rotary part
+    const uint64_t rows = (uint64_t)pool->num_blocks * pool->block_size;
+    const uint32_t box = pool->block_size < kTok ? pool->block_size : kTok;
+    const uint64_t rdims[4] = {64, 8, (uint64_t)pool->latent_dim / 64, rows / 8};
+    const uint64_t rstrides[3] = {width * 2, 128, width * 16};
+    const uint32_t rbox[4] = {64, 8, pool->latent_dim % 256 == 0 ? 4u : 2u, box / 8};
+    const uint64_t pdims[2] = {width, rows};
+    const uint32_t pbox[2] = {64, box};
+    if (!encode_bf16_map_sw128(&mq, q, 2, qdims, strides, qbox) ||
+        !encode_bf16_map_sw128(&mr, pool->rows, 4, rdims, rstrides, rbox) ||
+        !encode_bf16_map_sw128(&mp, pool->rows, 2, pdims, strides, pbox))
+        return cudaErrorInvalidValue;
+    switch (p.R / 16) {
+        case 1: return launch_rows<16>(p, mq, mr, mp, stream);
+        case 2: return launch_rows<32>(p, mq, mr, mp, stream);
+        case 3: return launch_rows<48>(p, mq, mr, mp, stream);
+        default: return launch_rows<64>(p, mq, mr, mp, stream);
+    }
+}
+
 static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t heads,
                            const int32_t* starts, const int32_t* tables, int32_t max_blocks,
                            const int32_t* lens, int32_t seqs, int32_t max_q, int32_t total_q,
                            int32_t max_context, float scale, int causal, void* out, void* workspace,
                            size_t workspace_bytes, int32_t* d_err, cudaStream_t stream) {
-    const Shape sh = shape_of(pool, heads, seqs, starts != nullptr, max_q, total_q, max_context);
+    const Shape sh = shape_of(pool, heads, seqs, max_q, total_q, max_context);
     if (workspace == nullptr || workspace_bytes < sh.bytes || !aligned16(workspace))
         return PA_ERR_INVALID_ARG;
     Params p;
@@ -889,9 +701,11 @@ static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t he
     p.max_context = max_context;
     p.causal = causal;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.siblings = sh.siblings;
     p.unit_rows = sh.unit_rows;
     p.R = sh.R;
+    // unit_rows / heads tokens more a unit, 64 tokens a tile: a tile more every `step` units
+    p.step = sh.unit_rows > 64 && heads > 1 ? heads / 2 : heads;
+    p.more = sh.unit_rows > 64 && heads == 1 ? 2 : 1;
     p.groups = sh.groups;
     p.min_tiles = 2;
     p.out = (uint16_t*)out;
@@ -900,35 +714,13 @@ static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t he
     p.parts = (float*)((char*)workspace + sh.meta_bytes + sh.stats_bytes);
     p.d_err = d_err;
 
-    const uint64_t width = pool->latent_dim + pool->rope_dim;
-    CUtensorMap mq, mr, mp;
-    const uint64_t qdims[2] = {width, (uint64_t)total_q * heads};
-    const uint64_t strides[1] = {width * 2};
-    const uint32_t qbox[2] = {64, (uint32_t)sh.R};
-    // the pool as [rows / 8][blocks of 64 dims][8][64], and as rows for the rotary part
-    const uint64_t rows = (uint64_t)pool->num_blocks * pool->block_size;
-    const uint32_t box = pool->block_size < kTok ? pool->block_size : kTok;
-    const uint64_t rdims[4] = {64, 8, (uint64_t)pool->latent_dim / 64, rows / 8};
-    const uint64_t rstrides[3] = {width * 2, 128, width * 16};
-    const uint32_t rbox[4] = {64, 8, pool->latent_dim % 256 == 0 ? 4u : 2u, box / 8};
-    const uint64_t pdims[2] = {width, rows};
-    const uint32_t pbox[2] = {64, box};
-    if (!encode_bf16_map_sw128(&mq, q, 2, qdims, strides, qbox) ||
-        !encode_bf16_map_sw128(&mr, pool->rows, 4, rdims, rstrides, rbox) ||
-        !encode_bf16_map_sw128(&mp, pool->rows, 2, pdims, strides, pbox))
-        return PA_ERR_CUDA;
-    cudaError_t e = cudaErrorInvalidValue;
-    switch (sh.R / 16) {
-        case 1: e = launch_rows<16>(p, mq, mr, mp, stream); break;
-        case 2: e = launch_rows<32>(p, mq, mr, mp, stream); break;
-        case 3: e = launch_rows<48>(p, mq, mr, mp, stream); break;
-        case 4: e = launch_rows<64>(p, mq, mr, mp, stream); break;
-    }
+    const int64_t q_rows = (int64_t)total_q * heads;
+    cudaError_t e = sh.pair ? launch_pair(p, q, pool, q_rows, stream) : launch_one(p, q, pool, q_rows, stream);
     if (e == cudaSuccess && sh.groups > 1) {
         // parts of one unit: about groups / sequences of them; many share a row's columns
         const int columns = pool->latent_dim / 4;
         const int shares = sh.groups >= 8 * seqs ? 512 / columns : 1;
-        e = launch_pdl(latent_merge_kernel, dim3((unsigned)sh.R, (unsigned)(sh.groups * sh.siblings)),
+        e = launch_pdl(latent_merge_kernel, dim3((unsigned)sh.R, (unsigned)sh.groups),
                        dim3((unsigned)(columns * shares)), 0, stream, p);
     }
     if (e != cudaSuccess) {
@@ -963,7 +755,7 @@ extern "C" pa_status pa_decode_latent_workspace_bytes(const pa_latent_pool* pool
     if (st != PA_OK) return st;
     *bytes = num_seqs == 0 || max_context == 0
                  ? 0
-                 : lat::shape_of(pool, num_q_heads, num_seqs, false, 1, num_seqs, max_context).bytes;
+                 : lat::shape_of(pool, num_q_heads, num_seqs, 1, num_seqs, max_context).bytes;
     return PA_OK;
 }
 
@@ -993,7 +785,7 @@ extern "C" pa_status pa_prefill_latent_workspace_bytes(const pa_latent_pool* poo
     if ((int64_t)total_q * num_q_heads > INT32_MAX) return PA_ERR_UNSUPPORTED;
     *bytes = num_seqs == 0 || total_q == 0 || max_q_len == 0 || max_context == 0
                  ? 0
-                 : lat::shape_of(pool, num_q_heads, num_seqs, true, max_q_len, total_q, max_context).bytes;
+                 : lat::shape_of(pool, num_q_heads, num_seqs, max_q_len, total_q, max_context).bytes;
     return PA_OK;
 }
 
