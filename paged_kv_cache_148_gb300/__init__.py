@@ -603,11 +603,11 @@ def _need_heads(t: torch.Tensor, name: str, dtype, device, tokens: int, heads: i
     """t [tokens][heads][dim], a token's elements contiguous; returns the token stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.device != device:
         raise ValueError("%s must live on %s, got %s" % (name, device, t.device))
-    if t.dim() != 3 or t.shape != (tokens, heads, dim):
+    if t.shape != (tokens, heads, dim):
         raise ValueError("%s must have shape %s, got %s"
                          % (name, (tokens, heads, dim), tuple(t.shape)))
     st, sh, sd = t.stride()
@@ -616,18 +616,42 @@ def _need_heads(t: torch.Tensor, name: str, dtype, device, tokens: int, heads: i
     return st if tokens > 1 else heads * dim
 
 
+def _fits(t, dtype, index: int, shape) -> bool:
+    """The usual case of an argument: a contiguous tensor of this type, device and shape."""
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index
+            and t.shape == shape and t.is_contiguous())
+
+
+def _want(t, name: str, dtype, device, index: int, shape):
+    """_fits, or the error that says why not."""
+    if not _fits(t, dtype, index, shape):
+        _need(t, name, dtype, device)
+        _need_shape(t, name, shape)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class _On:
-    """The device and stream of a call: `stream`, or the current one of the tensors' device."""
+    """The device and stream of a call: `stream`, or the current one of the tensors' device.
+
+    handle is the raw stream; made(t) marks a tensor that the call itself made as used on
+    `stream`, so that its memory is not reused before `stream` is done with it.
+    """
 
     __slots__ = ("guard", "handle", "stream")
 
-    def __init__(self, device, stream):
-        self.guard = None
-        if device.type == "cuda" and device.index is not None \
-                and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
+    def __init__(self, device, index: int, stream):
+        if index < 0:
+            raise ValueError("tensors must live on a CUDA device, got %s" % device)
+        self.guard = None if torch.cuda.current_device() == index else torch.cuda.device(index)
         self.stream = stream
-        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+        if stream is not None:
+            self.handle = stream.cuda_stream
+        elif _raw_stream is not None:
+            self.handle = _raw_stream(index)
+        else:
+            self.handle = torch.cuda.current_stream(index).cuda_stream
 
     def __enter__(self):
         if self.guard is not None:
@@ -639,8 +663,7 @@ class _On:
             self.guard.__exit__(*exc)
 
     def made(self, t):
-        """A tensor made by the call itself: its memory waits for `stream` too before it is reused."""
-        if t is not None and self.stream is not None:
+        if self.stream is not None:
             t.record_stream(self.stream)
         return t
 
@@ -655,28 +678,26 @@ def rope_write_kv(pool: KVPool, q: Optional[torch.Tensor], k_new: torch.Tensor,
     q, k_new and v_new may be slices of one projection (any token stride).  q None
     writes K and V alone; q_out may be q.
     """
-    T = int(slot_mapping.shape[0])
-    dev, io, D = pool.device, pool.io_dtype, pool.head_dim
-    ks = _need_heads(k_new, "k_new", io, dev, T, pool.num_kv_heads, D)
-    vs = _need_heads(v_new, "v_new", io, dev, T, pool.num_kv_heads, D)
-    _need(positions, "positions", torch.int64, dev)
-    _need(slot_mapping, "slot_mapping", torch.int64, dev)
-    _need_shape(positions, "positions", (T,))
-    _need_shape(slot_mapping, "slot_mapping", (T,))
+    T = slot_mapping.shape[0]
+    dev, io, D, Hkv = pool.device, pool.io_dtype, pool.head_dim, pool.num_kv_heads
+    index = pool.k.get_device()
+    ks = _need_heads(k_new, "k_new", io, dev, T, Hkv, D)
+    vs = _need_heads(v_new, "v_new", io, dev, T, Hkv, D)
+    _want(positions, "positions", torch.int64, dev, index, (T,))
+    _want(slot_mapping, "slot_mapping", torch.int64, dev, index, (T,))
     _need_err(d_err, dev)
     _need_rope(rope, dev)
     Hq = qs = 0
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be a tensor [T][H_q][D]")
-        Hq = int(q.shape[1])
+        Hq = q.shape[1]
         qs = _need_heads(q, "q", io, dev, T, Hq, D)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if q_out is not None:
-        _need(q_out, "q_out", io, dev)
-        _need_shape(q_out, "q_out", (T, Hq, D))
-    with _On(dev, stream) as on:
+        _want(q_out, "q_out", io, dev, index, (T, Hq, D))
+    with _On(dev, index, stream) as on:
         if q is not None and q_out is None:
             q_out = on.made(torch.empty((T, Hq, D), dtype=io, device=dev))
         _check(lib().pa_rope_write_kv(pool.c, rope.c, q.data_ptr() if Hq else None, qs, Hq,
@@ -716,6 +737,8 @@ class LatentPool:
         _need(self.rows, "rows", dtype)
         _need_shape(self.rows, "rows", shape)
         self.device = self.rows.device
+        self._index = self.rows.get_device()
+        self._bytes = {}  # workspace bytes by shape of a call
         self._c = pa_latent_pool(self.rows.data_ptr(), self.num_blocks, self.block_size,
                                  self.latent_dim, self.rope_dim, DTYPE_BF16)
         self.c = ctypes.byref(self._c)
@@ -737,37 +760,34 @@ def write_latent(pool: LatentPool, latent: torch.Tensor, k_rope: torch.Tensor,
     latent, k_rope and q_rope may be slices of wider projections (any token and head
     stride that is a multiple of 16 bytes).
     """
-    T, dev = int(slot_mapping.shape[0]), pool.device
-    for t, name, dim in ((latent, "latent", pool.latent_dim), (k_rope, "k_rope", pool.rope_dim)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 2:
-            raise ValueError("%s must be a tensor [T][%d]" % (name, dim))
-    ls = _need_heads(latent.unsqueeze(1), "latent", pool.dtype, dev, T, 1, pool.latent_dim)
-    ks = _need_heads(k_rope.unsqueeze(1), "k_rope", pool.dtype, dev, T, 1, pool.rope_dim)
-    _need(positions, "positions", torch.int64, dev)
-    _need(slot_mapping, "slot_mapping", torch.int64, dev)
-    _need_shape(positions, "positions", (T,))
-    _need_shape(slot_mapping, "slot_mapping", (T,))
+    T, dev, index = slot_mapping.shape[0], pool.device, pool._index
+    ls = _need_rows(latent, "latent", pool.dtype, dev, T, pool.latent_dim)
+    ks = _need_rows(k_rope, "k_rope", pool.dtype, dev, T, pool.rope_dim)
+    _want(positions, "positions", torch.int64, dev, index, (T,))
+    _want(slot_mapping, "slot_mapping", torch.int64, dev, index, (T,))
     _need_err(d_err, dev)
     _need_rope(rope, dev)
     if (q_rope is None) != (q is None):
         raise ValueError("q_rope and q come together")
     H = qs = qh = 0
     if q is not None:
-        _need(q, "q", pool.dtype, dev)
-        if q.dim() != 3:
-            raise ValueError("q must be [T][H][%d]" % pool.width)
-        H = int(q.shape[1])
-        _need_shape(q, "q", (T, H, pool.width))
-        if not isinstance(q_rope, torch.Tensor) or q_rope.dtype != pool.dtype:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a tensor [T][H][%d]" % pool.width)
+        H = q.shape[1]
+        _want(q, "q", pool.dtype, dev, index, (T, H, pool.width))
+        if not isinstance(q_rope, torch.Tensor) or q_rope.dtype is not pool.dtype:
             raise TypeError("q_rope must be a %s tensor" % pool.dtype)
         if q_rope.device != dev:
             raise ValueError("q_rope must live on %s, got %s" % (dev, q_rope.device))
         _need_shape(q_rope, "q_rope", (T, H, pool.rope_dim))
-        if q_rope.stride(2) != 1 and pool.rope_dim > 1:
+        qs, qh, qd = q_rope.stride()
+        if qd != 1:
             raise ValueError("each head of q_rope must be contiguous")
-        qh = q_rope.stride(1) if H > 1 else pool.rope_dim
-        qs = q_rope.stride(0) if T > 1 else max((H - 1) * qh + pool.rope_dim, 0)
-    with _On(dev, stream) as on:
+        if H <= 1:
+            qh = pool.rope_dim
+        if T <= 1:
+            qs = max((H - 1) * qh + pool.rope_dim, 0)
+    with _On(dev, index, stream) as on:
         _check(lib().pa_write_latent(pool.c, rope.c, latent.data_ptr(), ls, k_rope.data_ptr(), ks,
                                      positions.data_ptr(), slot_mapping.data_ptr(), T,
                                      q_rope.data_ptr() if H else None, qs, qh, H,
@@ -777,17 +797,30 @@ def write_latent(pool: LatentPool, latent: torch.Tensor, k_rope: torch.Tensor,
     return q
 
 
+def _need_rows(t: torch.Tensor, name: str, dtype, device, tokens: int, dim: int):
+    """t [tokens][dim], a token's elements contiguous; returns the token stride."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("%s must be a tensor [T][%d]" % (name, dim))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s must live on %s, got %s" % (name, device, t.device))
+    _need_shape(t, name, (tokens, dim))
+    st, sd = t.stride()
+    if sd != 1 and dim > 1:
+        raise ValueError("each token of %s must be contiguous" % name)
+    return st if tokens > 1 else dim
+
+
 def copy_latent_blocks(pool: LatentPool, src: torch.Tensor, dst: torch.Tensor,
                        d_err: Optional[torch.Tensor] = None, stream=None):
     """Block copy dst[i] <- src[i] (int32 device tensors) in a latent pool."""
-    _need(src, "src", torch.int32, pool.device)
-    _need(dst, "dst", torch.int32, pool.device)
-    if src.shape != dst.shape or src.dim() != 1:
-        raise ValueError("src and dst must be 1-D of equal length")
+    n = src.numel()
+    _want(src, "src", torch.int32, pool.device, pool._index, (n,))
+    _want(dst, "dst", torch.int32, pool.device, pool._index, (n,))
     _need_err(d_err, pool.device)
-    with _On(pool.device, stream) as on:
-        _check(lib().pa_copy_latent_blocks(pool.c, src.data_ptr(), dst.data_ptr(),
-                                           int(src.shape[0]),
+    with _On(pool.device, pool._index, stream) as on:
+        _check(lib().pa_copy_latent_blocks(pool.c, src.data_ptr(), dst.data_ptr(), n,
                                            None if d_err is None else d_err.data_ptr(), on.handle),
                "pa_copy_latent_blocks")
 
@@ -824,23 +857,38 @@ def prefill_latent_workspace(pool: LatentPool, num_seqs: int, num_q_heads: int, 
     return torch.empty(n, dtype=torch.uint8, device=pool.device) if n > 0 else None
 
 
-def _need_latent_q(pool, q, block_tables, context_lens, out):
-    _need(q, "q", pool.dtype, pool.device)
-    _need(block_tables, "block_tables", torch.int32, pool.device)
-    _need(context_lens, "context_lens", torch.int32, pool.device)
-    if q.dim() != 3 or q.shape[2] != pool.width:
+def _bytes_of(pool, fn, *shape) -> int:
+    """fn(pool, *shape), remembered for the shapes that a program calls again."""
+    n = pool._bytes.get(shape)
+    if n is None:
+        if len(pool._bytes) >= 256:
+            pool._bytes.clear()
+        n = pool._bytes[shape] = fn(pool, *shape)
+    return n
+
+
+def _need_latent_q(pool, q, block_tables, context_lens, out, d_err, workspace):
+    """Checks of a latent attention's arguments; returns T, H, B and the table's width."""
+    dev, index = pool.device, pool._index
+    if not (isinstance(q, torch.Tensor) and isinstance(block_tables, torch.Tensor)
+            and isinstance(context_lens, torch.Tensor)):
+        raise TypeError("q, block_tables and context_lens must be tensors")
+    if q.dim() != 3:
         raise ValueError("q must be [T][H][%d], got %s" % (pool.width, tuple(q.shape)))
     if context_lens.dim() != 1:
         raise ValueError("context_lens must be 1-D")
-    B = int(context_lens.shape[0])
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("block_tables must be [%d][max_blocks], got %s"
-                         % (B, tuple(block_tables.shape)))
-    T, H = int(q.shape[0]), int(q.shape[1])
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be 2-D")
+    T, H, _ = q.shape
+    B, width = context_lens.shape[0], block_tables.shape[1]
+    _want(q, "q", pool.dtype, dev, index, (T, H, pool.width))
+    _want(context_lens, "context_lens", torch.int32, dev, index, (B,))
+    _want(block_tables, "block_tables", torch.int32, dev, index, (B, width))
     if out is not None:
-        _need(out, "out", pool.dtype, pool.device)
-        _need_shape(out, "out", (T, H, pool.latent_dim))
-    return T, H, B
+        _want(out, "out", pool.dtype, dev, index, (T, H, pool.latent_dim))
+    _need_err(d_err, dev)
+    _need_workspace(workspace, dev)
+    return T, H, B, width
 
 
 def decode_latent(pool: LatentPool, q: torch.Tensor, block_tables: torch.Tensor,
@@ -853,21 +901,19 @@ def decode_latent(pool: LatentPool, q: torch.Tensor, block_tables: torch.Tensor,
     rotated part behind it (write_latent).  workspace: decode_latent_workspace(); one is
     made where it is missing or too small.
     """
-    T, H, B = _need_latent_q(pool, q, block_tables, context_lens, out)
+    T, H, B, width = _need_latent_q(pool, q, block_tables, context_lens, out, d_err, workspace)
     if T != B:
         raise ValueError("q must hold one token a sequence: %d, got %d" % (B, T))
-    _need_workspace(workspace, pool.device)
-    _need_err(d_err, pool.device)
-    need = decode_latent_workspace_bytes(pool, B, H, int(max_context))
-    with _On(pool.device, stream) as on:
+    max_context = int(max_context)
+    need = _bytes_of(pool, decode_latent_workspace_bytes, B, H, max_context)
+    with _On(pool.device, pool._index, stream) as on:
         if out is None:
             out = on.made(torch.empty((T, H, pool.latent_dim), dtype=pool.dtype, device=pool.device))
-        have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        have = 0 if workspace is None else workspace.nbytes
         if have < need:
             workspace, have = on.made(torch.empty(need, dtype=torch.uint8, device=pool.device)), need
-        _check(lib().pa_decode_latent(pool.c, q.data_ptr(), H, block_tables.data_ptr(),
-                                      int(block_tables.shape[1]), context_lens.data_ptr(), B,
-                                      int(max_context), float(scale), out.data_ptr(),
+        _check(lib().pa_decode_latent(pool.c, q.data_ptr(), H, block_tables.data_ptr(), width,
+                                      context_lens.data_ptr(), B, max_context, scale, out.data_ptr(),
                                       workspace.data_ptr() if have else None, have,
                                       None if d_err is None else d_err.data_ptr(), on.handle),
                "pa_decode_latent")
@@ -882,22 +928,19 @@ def prefill_latent(pool: LatentPool, q: torch.Tensor, cu_seqlens_q: torch.Tensor
     """Latent attention of several new tokens a sequence, absorbed form; returns out
     [T][H][latent_dim] bf16.  q: [T][H][latent_dim + rope_dim], sequence s at
     cu_seqlens_q[s] .. cu_seqlens_q[s + 1]; its tokens' rows are already written."""
-    T, H, B = _need_latent_q(pool, q, block_tables, context_lens, out)
-    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, pool.device)
-    _need_shape(cu_seqlens_q, "cu_seqlens_q", (B + 1,))
-    _need_workspace(workspace, pool.device)
-    _need_err(d_err, pool.device)
-    need = prefill_latent_workspace_bytes(pool, B, H, T, int(max_q_len), int(max_context))
-    with _On(pool.device, stream) as on:
+    T, H, B, width = _need_latent_q(pool, q, block_tables, context_lens, out, d_err, workspace)
+    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, pool.device, pool._index, (B + 1,))
+    max_q_len, max_context = int(max_q_len), int(max_context)
+    need = _bytes_of(pool, prefill_latent_workspace_bytes, B, H, T, max_q_len, max_context)
+    with _On(pool.device, pool._index, stream) as on:
         if out is None:
             out = on.made(torch.empty((T, H, pool.latent_dim), dtype=pool.dtype, device=pool.device))
-        have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        have = 0 if workspace is None else workspace.nbytes
         if have < need:
             workspace, have = on.made(torch.empty(need, dtype=torch.uint8, device=pool.device)), need
         _check(lib().pa_prefill_latent(pool.c, q.data_ptr(), T, H, cu_seqlens_q.data_ptr(),
-                                       context_lens.data_ptr(), block_tables.data_ptr(),
-                                       int(block_tables.shape[1]), B, int(max_q_len),
-                                       int(max_context), float(scale), 1 if causal else 0,
+                                       context_lens.data_ptr(), block_tables.data_ptr(), width, B,
+                                       max_q_len, max_context, scale, 1 if causal else 0,
                                        out.data_ptr(), workspace.data_ptr() if have else None, have,
                                        None if d_err is None else d_err.data_ptr(), on.handle),
                "pa_prefill_latent")

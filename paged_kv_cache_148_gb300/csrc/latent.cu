@@ -79,7 +79,8 @@ struct Bars {
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint32_t tmem_base;
     int32_t abort;
-    uint32_t valid[4];               // pages of a tile that were loaded, by tile mod 4
+    uint64_t info[kInfo];
+    uint32_t valid[kInfo];           // pages of a tile that were loaded, by tile
     float factor[64];                // rescaling factors of the rows
     float inv[2][64];                // one over the rows' sums, by unit mod 2
     Scan scan;
@@ -146,10 +147,11 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             mbar_init(&bars->rope_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->s_full[i], 2);
+            mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->p_full[i], 128);
             mbar_init(&bars->pv_done[i], 1);
         }
+        for (int i = 0; i < kInfo; ++i) mbar_init(&bars->info[i], 1);
         bars->abort = 0;
         fence_mbar_init();
         tc::prefetch_tmap(&tmap_q);
@@ -164,12 +166,13 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     griddep_launch();
 
     int64_t per;
-    Line line = find_stretch<kThreads>(p, group, blockIdx.x == 0, bars->scan, per);
+    Line line;
+    Part w;
+    const bool some = find_stretch<kThreads>(p, group, blockIdx.x == 0, bars->scan, line, w, per);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = bars->tmem_base;
-    Part w;
 
     const uint32_t tP = smem_u32(smem + L::kP);
     const uint32_t tRing = smem_u32(smem + L::kRing);
@@ -183,8 +186,8 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const int pages = kTok / box;                // boxes of one tile
         bool ok = true;
         uint32_t part_n = 0, rope_n = 0, q_n = 0;    // loads issued so far
-        int64_t it = 0;
-        for (int unit = 0; ok && next_part(p, line, w); ++unit) {
+        uint32_t it = 0;
+        for (int unit = 0; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
             auto fetch = [&](int t) -> int32_t {     // this lane's page of tile t; -1 past the end
                 const int64_t pos = (int64_t)t * kTok + lane * box;
@@ -192,7 +195,17 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 const int64_t e = pos >> p.log2_bp;
                 return e < p.max_blocks ? max(__ldg(table + e), -1) : p.num_blocks;
             };
+            auto load_q = [&] {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars->q_full, (2 * PAIRS + 1) * R * 128);
+                    for (int b = 0; b <= 2 * PAIRS; ++b)
+                        tc::tma_load_2d(smem + b * R * 128, &tmap_q, b * 64, w.row, &bars->q_full);
+                }
+                __syncwarp();
+                ++q_n;
+            };
             int32_t next = fetch(w.t0);
+            if (unit == 0) load_q();
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const int32_t id = next;
                 next = fetch(t + 1);
@@ -223,7 +236,8 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     break;
                 uint64_t* bar = &bars->rope_full[slot];
                 if (lane == 0) {
-                    bars->valid[it & 3] = mask;
+                    bars->valid[it % kInfo] = mask;
+                    mbar_arrive(&bars->info[it % kInfo]);
                     mbar_arrive_expect_tx(bar, bytes);
                 }
                 __syncwarp();
@@ -231,15 +245,9 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     tc::tma_load_2d(smem + L::kRope + slot * kBlock + lane * box * 128, &tmap_rope,
                                     kDim, row, bar);
                 ++rope_n;
-                if (t == w.t0) {  // Q behind the unit's first tile: it waits for the unit before
-                    if (unit > 0 && !(ok = wait_warp(&bars->q_empty, (unit - 1) & 1, bars, p.d_err))) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&bars->q_full, (2 * PAIRS + 1) * R * 128);
-                        for (int b = 0; b <= 2 * PAIRS; ++b)
-                            tc::tma_load_2d(smem + b * R * 128, &tmap_q, b * 64, w.row, &bars->q_full);
-                    }
-                    __syncwarp();
-                    ++q_n;
+                if (t == w.t0 && unit > 0) {  // Q behind the unit's first tile: it waits for the unit before
+                    if (!(ok = wait_warp(&bars->q_empty, (unit - 1) & 1, bars, p.d_err))) break;
+                    load_q();
                 }
             }
         }
@@ -253,11 +261,6 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ S
-        // An MMA's operands sit in warp-uniform registers.  Trip counts and branches
-        // come from votes, whose results the compiler knows to be uniform, and all
-        // offsets within a tile are constants: issue then keeps up with the tensor
-        // core (with descriptors from general registers each MMA took 100 cycles to
-        // issue, against 32 to 48 to run).
         constexpr uint32_t idesc = tc::idesc_bf16_f32(64, kTok, 0, 0);
         constexpr uint64_t q_block = (uint64_t)(R * 128) >> 4;
         const uint64_t dq = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
@@ -266,7 +269,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const int rope_steps = p.rope_dim >> 4;
         uint32_t slot = 0, phase = 0, slot_r = 0, phase_r = 0, it = 0;
         bool ok = true;
-        for (int unit = 0; ok && __any_sync(0xffffffffu, next_part(p, line, w)); ++unit) {
+        for (int unit = 0; ok && __any_sync(0xffffffffu, unit == 0 ? some : next_part(p, line, w)); ++unit) {
             const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
             if (!(ok = wait_warp(&bars->q_full, unit & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
@@ -295,11 +298,9 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 for (int k = 0; k < 4; ++k)
                     if (k < rope_steps)
                         tc::mma_ss_warp(d, dq + 2 * PAIRS * q_block + k * 2, b + k * 2, idesc, 1u);
+                tc::commit_warp(&bars->s_full[it & 1]);
                 tc::commit_warp(&bars->rope_empty[slot_r]);
                 if (t + 1 == n) tc::commit_warp(&bars->q_empty);
-                tc::commit_warp(&bars->s_full[it & 1]);
-                if (lane == 0) mbar_arrive(&bars->s_full[it & 1]);  // hands on valid[] too
-                __syncwarp();
                 if (++slot_r == L::kRopeSlots) {
                     slot_r = 0;
                     phase_r ^= 1;
@@ -314,22 +315,22 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const uint64_t dp = tc::smem_desc_sw128(tP, 16, 1024);
         uint32_t slot = 0, it = 0;
         bool ok = true;
-        for (int unit = 0; ok && __any_sync(0xffffffffu, next_part(p, line, w)); ++unit) {
+        for (int unit = 0; ok && __any_sync(0xffffffffu, unit == 0 ? some : next_part(p, line, w)); ++unit) {
             const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
             if (unit > 0 && !(ok = wait_warp(&bars->o_free, (unit - 1) & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
                 if (!(ok = wait_warp(&bars->p_full[it & 1], (it >> 1) & 1, bars, p.d_err))) break;
                 tc::fence_after_sync();
                 const uint64_t b = dp + (uint64_t)((it & 1) * (L::kPBytes >> 4));
-                const uint32_t first = t > 0 ? 1u : 0u;
+                const uint32_t more = t > 0 ? 1u : 0u;
 #pragma unroll
                 for (int m = 0; m < PAIRS; ++m) {
-                    constexpr int per = L::C / 2;            // pairs of a part
+                    constexpr int per = L::C / 2;                // pairs of a part
                     const uint64_t a = dv + (uint64_t)(slot * (L::kPart >> 4) + m % per * (2048 >> 4));
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc::mma_ss_warp(tmem + 128 + m * R, a + (k * 2 * L::C * 1024 >> 4), b + (k * 32 >> 4), idesc,
-                                        k > 0 ? 1u : first);
+                                        k > 0 ? 1u : more);
                     if (m % per == per - 1) {
                         tc::commit_warp(&bars->part_empty[slot]);
                         if (++slot == L::kSlots) slot = 0;
@@ -352,7 +353,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         // limit, so none may stay away)
         bool ok = true;
         int32_t chain_rows = 0, chain_row = 0, chain = 0;
-        for (int unit = 0; next_part(p, line, w); ++unit) {
+        for (int unit = 0; unit == 0 ? some : next_part(p, line, w); ++unit) {
             int lim0 = 0, lim1 = 0;                    // tokens that the two rows see
             if (r0 < w.rows) lim0 = p.causal ? w.q.n - w.q.fresh + (w.token + r0) / p.heads + 1 : w.q.n;
             if (r1 < w.rows) lim1 = p.causal ? w.q.n - w.q.fresh + (w.token + r1) / p.heads + 1 : w.q.n;
@@ -362,11 +363,12 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const int b = (int)(it & 1);
+                ok &= wait_warp(&bars->info[it % kInfo], (it / kInfo) & 1, bars, p.d_err);
                 ok &= wait_warp(&bars->s_full[b], (it >> 1) & 1, bars, p.d_err);
                 tc::fence_after_sync();
                 const int pos = t * kTok;
                 const int boxes = kTok >> log2_box;
-                const uint32_t valid = *(volatile uint32_t*)&bars->valid[it & 3];
+                const uint32_t valid = *(volatile uint32_t*)&bars->valid[it % kInfo];
                 const bool whole = valid == (0xffffffffu >> (32 - boxes)) && pos + kTok <= ctx;
                 uint32_t s[32];
                 float t0 = -INFINITY, t1 = -INFINITY;
@@ -538,53 +540,147 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     }
 }
 
-// Joins the parts of one cut unit: out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// Block (row, stretch in which the unit begins); part 0 is that stretch's last,
-// part i the first of the i-th stretch behind it.  A thread holds four dims and
-// every gridlike share of the parts; the shares meet in shared memory.
-__global__ void __launch_bounds__(512) latent_merge_kernel(const Params p) {
+// Joins the parts of a cut unit: out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// meta[g] names the unit that begins in stretch g and goes on behind it: its part
+// 0 is that stretch's last, part i the first of the i-th stretch behind it.  Both
+// kernels are bound by the latency of their loads (meta, then statistics and
+// parts), so the parts' are issued before the statistics are looked at.
+PA_DEVICE int64_t part_slot(int g, int i) { return ((int64_t)g + i) * 2 + (i == 0 ? 1 : 0); }
+
+// The j-th cut unit of the call (blockDim.x >= groups): its meta and stretch.
+PA_DEVICE int4 find_cut(const Params& p, int j, int& g) {
+    __shared__ int counts[16];
+    __shared__ int found;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 meta = (int)threadIdx.x < p.groups ? p.meta[threadIdx.x] : make_int4(0, 0, 0, 0);
+    const uint32_t cut = __ballot_sync(0xffffffffu, meta.x >= 2);
+    if (threadIdx.x == 0) found = -1;
+    if (lane == 0) counts[warp] = __popc(cut);
+    __syncthreads();
+    int before = __popc(cut & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) before += counts[w];
+    if (meta.x >= 2 && before == j) found = threadIdx.x;
+    __syncthreads();
+    g = found;
+    return g >= 0 ? p.meta[g] : make_int4(0, 0, 0, 0);
+}
+
+PA_DEVICE void add_scaled(float4& a, float f, const float4& x) {
+    a.x += f * x.x;
+    a.y += f * x.y;
+    a.z += f * x.z;
+    a.w += f * x.w;
+}
+
+PA_DEVICE void store_row(const Params& p, int row, int col, const float4& a, float l) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    reinterpret_cast<uint2*>(p.out + (int64_t)row * p.latent_dim)[col] =
+        make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+}
+
+// Few parts a unit: a warp a row, K float4 columns a lane, all rows of all units at
+// once (64 contexts on 128 heads: 5 us; a block a row went through the machine in
+// four waves of three latencies, 14 us).
+template <int K>
+__global__ void __launch_bounds__(256) latent_merge_few_kernel(const Params p) {
     griddep_wait();
-    const int4 meta = p.meta[blockIdx.y];
-    if (meta.x < 2 || (int)blockIdx.x >= meta.z) return;
+    griddep_launch();
+    const int g = blockIdx.y, r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int4 meta = p.meta[g];
+    if (meta.x < 2 || r >= meta.z) return;
+    auto part = [&](int i) { return reinterpret_cast<const float4*>(p.parts + (part_slot(g, i) * p.R + r) * p.latent_dim) + lane; };
+    auto stat = [&](int i) { return p.stats[part_slot(g, i) * p.R + r]; };
+    float4 o[2][K];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 0; k < K; ++k) o[e][k] = part(e)[32 * k];
+    float top = -INFINITY;
+    for (int i = 0; i < meta.x; ++i) top = fmaxf(top, stat(i).x);
+    float4 acc[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int i = 0; i < meta.x; i += 2) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (i + e >= meta.x) break;
+            const float2 st = stat(i + e);
+            const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
+            l += f * st.y;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                add_scaled(acc[k], f, o[e][k]);
+                if (i + 2 + e < meta.x) o[e][k] = part(i + 2 + e)[32 * k];
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) store_row(p, meta.y + r, lane + 32 * k, acc[k], l);
+}
+
+// Many parts a unit: a block a row; a thread has one float4 column of every
+// shares-th part, eight in flight, and the shares meet in shared memory.
+constexpr int kMergeParts = 256;     // at most one a stretch
+
+__global__ void __launch_bounds__(512) latent_merge_many_kernel(const Params p) {
+    griddep_wait();
+    griddep_launch();
     const int r = blockIdx.x;
-    const int group = blockIdx.y;
+    int g;
+    const int4 meta = find_cut(p, blockIdx.y, g);
+    if (meta.x < 2 || r >= meta.z) return;
+    const int n = min(meta.x, kMergeParts);
     const int columns = p.latent_dim >> 2;
     const int col = threadIdx.x % columns, share = threadIdx.x / columns, shares = blockDim.x / columns;
-    auto slot = [&](int i) -> int64_t {
-        return ((int64_t)group + i) * 2 + (i == 0 ? 1 : 0);
-    };
-    float top = -INFINITY;
-    for (int i = 0; i < meta.x; ++i) top = fmaxf(top, p.stats[slot(i) * p.R + r].x);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int i = share; i < meta.x; i += shares) {
-        const float2 st = p.stats[slot(i) * p.R + r];
-        const float4 o = reinterpret_cast<const float4*>(p.parts + (slot(i) * p.R + r) * p.latent_dim)[col];
-        const float f = st.x == -INFINITY ? 0.f : ex2(st.x - top);
-        l += f * st.y;
-        acc.x += f * o.x;
-        acc.y += f * o.y;
-        acc.z += f * o.z;
-        acc.w += f * o.w;
-    }
+    __shared__ float2 st[kMergeParts];
     __shared__ float4 sums[512];
-    __shared__ float ls[512];
+    float4 o[8];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = i0 + e * shares;
+            if (i < n) o[e] = reinterpret_cast<const float4*>(p.parts + (part_slot(g, i) * p.R + r) * p.latent_dim)[col];
+        }
+    };
+    load(share);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) st[i] = p.stats[part_slot(g, i) * p.R + r];
+    __syncthreads();
+    float top = -INFINITY, l = 0.f;
+    for (int i = 0; i < n; ++i) top = fmaxf(top, st[i].x);
+    for (int i = 0; i < n; ++i) l += st[i].x == -INFINITY ? 0.f : ex2(st[i].x - top) * st[i].y;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = share; i0 < n; i0 += 8 * shares) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = i0 + e * shares;
+            if (i < n) add_scaled(acc, st[i].x == -INFINITY ? 0.f : ex2(st[i].x - top), o[e]);
+        }
+        load(i0 + 8 * shares);
+    }
     sums[threadIdx.x] = acc;
-    ls[threadIdx.x] = l;
     __syncthreads();
     if (share > 0) return;
-    for (int i = 1; i < shares; ++i) {
-        const float4 o = sums[i * columns + col];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
-        l += ls[i * columns + col];
+    for (int i = 1; i < shares; ++i) add_scaled(acc, 1.f, sums[i * columns + col]);
+    store_row(p, meta.y + r, col, acc, l);
+}
+
+static cudaError_t launch_merge(const Params& p, int64_t units, cudaStream_t stream) {
+    // a unit is cut into groups / units parts or so
+    if (p.groups >= 6 * units) {
+        // a block for every unit, not for every stretch: empty ones would cost a launch each
+        const unsigned cuts = (unsigned)units;
+        const int columns = p.latent_dim / 4;
+        return launch_pdl(latent_merge_many_kernel, dim3((unsigned)p.R, cuts),
+                          dim3((unsigned)(512 / columns * columns)), 0, stream, p);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint2* dst = reinterpret_cast<uint2*>(p.out + (int64_t)(meta.y + r) * p.latent_dim) + col;
-    *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    const dim3 grid((unsigned)(p.R / 8), (unsigned)p.groups);
+    switch (p.latent_dim / 128) {
+        case 1: return launch_pdl(latent_merge_few_kernel<1>, grid, dim3(256), 0, stream, p);
+        case 2: return launch_pdl(latent_merge_few_kernel<2>, grid, dim3(256), 0, stream, p);
+        case 3: return launch_pdl(latent_merge_few_kernel<3>, grid, dim3(256), 0, stream, p);
+        default: return launch_pdl(latent_merge_few_kernel<4>, grid, dim3(256), 0, stream, p);
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -592,6 +688,7 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const Params p) {
 struct Shape {
     bool pair;
     int unit_rows, R, groups;
+    int64_t units;                     // at most
     size_t meta_bytes, stats_bytes, bytes;
 };
 
@@ -611,11 +708,13 @@ static Shape shape_of(const pa_latent_pool* pool, int heads, int seqs, int max_q
         s.R = (s.unit_rows + 15) / 16 * 16;
     }
     // a sequence's last unit may not be full, and the line holds up to two tiles more a unit
-    const int64_t units = (int64_t)total_q * heads / s.unit_rows + seqs;
-    const int64_t tiles = units * ((max_context + kTok - 1) / kTok + 2);
+    s.units = (int64_t)total_q * heads / s.unit_rows + seqs;
+    if (max_q == 1 && rows <= s.unit_rows) s.units = seqs;
+    const int64_t tiles = s.units * ((max_context + kTok - 1) / kTok + 2);
     const int64_t most = device_sm_count() / (s.pair ? 2 : 1);
     s.groups = (int)(tiles < most ? tiles : most);
     if (s.groups < 1) s.groups = 1;
+    if (s.groups > kMergeParts) s.groups = kMergeParts;
     const size_t slots = (size_t)2 * s.groups;
     s.meta_bytes = round256((size_t)s.groups * sizeof(int4));
     s.stats_bytes = round256(slots * s.R * sizeof(float2));
@@ -716,13 +815,7 @@ static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t he
 
     const int64_t q_rows = (int64_t)total_q * heads;
     cudaError_t e = sh.pair ? launch_pair(p, q, pool, q_rows, stream) : launch_one(p, q, pool, q_rows, stream);
-    if (e == cudaSuccess && sh.groups > 1) {
-        // parts of one unit: about groups / sequences of them; many share a row's columns
-        const int columns = pool->latent_dim / 4;
-        const int shares = sh.groups >= 8 * seqs ? 512 / columns : 1;
-        e = launch_pdl(latent_merge_kernel, dim3((unsigned)sh.R, (unsigned)sh.groups),
-                       dim3((unsigned)(columns * shares)), 0, stream, p);
-    }
+    if (e == cudaSuccess && sh.groups > 1) e = launch_merge(p, sh.units, stream);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return PA_ERR_CUDA;

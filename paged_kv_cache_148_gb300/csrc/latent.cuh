@@ -16,6 +16,10 @@ constexpr int kBlock = kTok * 128;   // bytes of 64 tokens x 64 elements
 constexpr float kRescale = 16.0f;
 constexpr int kSmemLimit = 232448;   // 227 KB
 
+// Rings of what the producer tells the softmax about a tile: it is at most kSlots + 2
+// tiles ahead of its slowest reader.
+constexpr int kInfo = 8;
+
 struct Params {
     int32_t num_blocks, log2_bp, latent_dim, rope_dim;
     int32_t heads;
@@ -73,30 +77,31 @@ struct Seq {
     int32_t start, fresh, n;   // first query token; query tokens; context
     int32_t units, first, step, more;  // tiles of unit u: first + more * (u / step); step 0: first
 
-    PA_DEVICE int64_t before(int64_t u) const {
-        if (step == 0) return u * first;
+    PA_DEVICE int64_t before(int u) const {
+        if (step == 0) return (int64_t)u * first;
         const int64_t k = u / step;
-        return u * first + more * (step * (k * (k - 1) / 2) + k * (u - k * step));
+        return (int64_t)u * first + more * (step * (k * (k - 1) / 2) + k * (u - k * step));
     }
 };
 
-template <bool REPORT>
-PA_DEVICE Seq read_seq(const Params& p, int s) {
+
+
+PA_DEVICE Seq read_seq(const Params& p, int s, bool report) {
     Seq q;
     q.units = q.first = q.step = q.more = 0;
     q.start = p.starts ? __ldg(p.starts + s) : s;
     q.fresh = p.starts ? __ldg(p.starts + s + 1) - q.start : 1;
     q.n = __ldg(p.lens + s);
     if (p.starts && (q.start < 0 || q.fresh < 0 || q.fresh > p.total_q - q.start)) {
-        if (REPORT) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
+        if (report) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
         return q;
     }
     if (q.fresh == 0 || (!p.starts && q.n <= 0)) return q;
     if (q.n < q.fresh) {
-        if (REPORT) set_error(p.d_err, PA_ERR_INVALID_ARG);
+        if (report) set_error(p.d_err, PA_ERR_INVALID_ARG);
         return q;
     }
-    if (REPORT && (q.n > p.max_context || q.fresh > p.max_q)) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
+    if (report && (q.n > p.max_context || q.fresh > p.max_q)) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
     const int64_t rows = (int64_t)min(q.fresh, p.max_q) * p.heads;
     q.units = (int)((rows + p.unit_rows - 1) / p.unit_rows);
     if (p.causal) {
@@ -132,20 +137,19 @@ struct Line {
 // The next share of the stretch, skipping places that the line holds too many.
 PA_DEVICE bool next_part(const Params& p, Line& l, Part& w) {
     while (l.at < l.end && l.s < p.seqs) {
-        const Seq q = read_seq<false>(p, l.s);
+        const Seq q = read_seq(p, l.s, false);
         const int64_t all = q.before(q.units);
         if (l.at >= l.seq_at + all) {
             l.seq_at += all;
             ++l.s;
             continue;
         }
-        int64_t lo = 0, hi = q.units - 1;  // last unit that begins at or before `at`
+        int u = 0, hi = q.units - 1;       // last unit that begins at or before `at`
         const int64_t off = l.at - l.seq_at;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) >> 1;
-            if (q.before(mid) <= off) lo = mid; else hi = mid - 1;
+        while (u < hi) {
+            const int mid = (int)(((unsigned)u + hi + 1) >> 1);
+            if (q.before(mid) <= off) u = mid; else hi = mid - 1;
         }
-        const int u = (int)lo;
         const int64_t begin = l.seq_at + q.before(u), stop = l.seq_at + q.before(u + 1);
         const int r0 = u * p.unit_rows;
         const int all_rows = min(q.fresh, p.max_q) * p.heads;
@@ -173,28 +177,28 @@ PA_DEVICE bool next_part(const Params& p, Line& l, Part& w) {
     return false;
 }
 
-// A block finds its stretch.  Every thread calls it; scratch is shared memory.
+// A block finds its stretch and the first share of it.  Every thread calls it;
+// scratch is shared memory.
 struct Scan {
     int64_t sums[8];
-    int64_t at;
-    int32_t seq;
+    Line line;
+    Part part;
+    int32_t some;
 };
 
 template <int THREADS>
-PA_DEVICE Line find_stretch(const Params& p, int group, bool report, Scan& sc, int64_t& per) {
+PA_DEVICE bool find_stretch(const Params& p, int group, bool report, Scan& sc, Line& line, Part& part,
+                            int64_t& per) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the line's length, then the sequence in which this stretch begins: each
     // thread adds up an equal run of sequences, and the one whose run holds the
     // stretch's first tile walks it
-    if (threadIdx.x == 0) {
-        sc.seq = p.seqs;
-        sc.at = 0;
-    }
+    if (threadIdx.x == 0) sc.some = 0;
     const int run = (p.seqs + THREADS - 1) / THREADS;
     const int s0 = min(p.seqs, (int)threadIdx.x * run), s1 = min(p.seqs, s0 + run);
     int64_t mine = 0;
     for (int s = s0; s < s1; ++s) {
-        const Seq q = report ? read_seq<true>(p, s) : read_seq<false>(p, s);
+        const Seq q = read_seq(p, s, report);
         mine += q.before(q.units);
     }
     int64_t upto = mine;
@@ -206,32 +210,28 @@ PA_DEVICE Line find_stretch(const Params& p, int group, bool report, Scan& sc, i
     if (lane == 31) sc.sums[warp] = upto;
     __syncthreads();
     int64_t total = 0, ahead = 0;
+#pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) ahead += sc.sums[w];
         total += sc.sums[w];
     }
-    per = max((total + p.groups - 1) / p.groups, (int64_t)p.min_tiles);
-    Line line;
+    const int64_t sum = total + p.groups - 1;
+    per = sum <= INT32_MAX ? (int64_t)((uint32_t)sum / (uint32_t)p.groups) : sum / p.groups;
+    per = max(per, (int64_t)p.min_tiles);
     line.at = min(total, group * per);
     line.end = min(total, line.at + per);
     ahead += upto - mine;
     if (line.at < line.end && ahead <= line.at && line.at < ahead + mine) {
-        int64_t at = ahead;
-        for (int s = s0; s < s1; ++s) {
-            const Seq q = read_seq<false>(p, s);
-            const int64_t all = q.before(q.units);
-            if (line.at < at + all) {
-                sc.seq = s;
-                sc.at = at;
-                break;
-            }
-            at += all;
-        }
+        line.s = s0;
+        line.seq_at = ahead;
+        sc.some = next_part(p, line, part);
+        sc.line = line;
+        sc.part = part;
     }
     __syncthreads();
-    line.s = sc.seq;
-    line.seq_at = sc.at;
-    return line;
+    line = sc.line;
+    part = sc.part;
+    return sc.some != 0;
 }
 
 // Tiles of the pair kernel (latent_pair.cu): units of up to 128 rows, a CTA pair each.

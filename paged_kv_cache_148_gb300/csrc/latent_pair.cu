@@ -14,8 +14,7 @@
 // every 256 dims, and a row's maximum, sum and scale are its lanes' own.
 //
 // Roles (256 threads, one CTA per SM): warp 0 loads Q and K, warp 7 V; warps 1 and
-// 6 of the leader issue S and O; warps 2-5 are softmax and epilogue: a thread has
-// one row and half of a tile's tokens.  K's barrier lies in the leader and counts
+// 6 of the leader issue S and O; warps 2-5 are softmax and epilogue: a thread has one row and half of a tile's tokens.  K's barrier lies in the leader and counts
 // both CTAs' bytes; V's is each CTA's own, and a CTA's P is only announced when its
 // V is there too.  Products are released to both CTAs by multicast commits.
 #include "latent.cuh"
@@ -27,7 +26,6 @@ namespace {
 
 constexpr int kPairThreads = 256;
 constexpr int kPairBars = 2048;
-constexpr int kValid = 8;
 
 template <int NJ>  // 256 dims each
 struct PairLayout {
@@ -50,8 +48,8 @@ struct PairBars {
     uint64_t q_full, q_empty, o_free;          // q_full, o_free, k_full, p_full: the leader's
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
     uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t info[kValid];
-    uint32_t valid[kValid];                    // slices of a tile that were loaded, by tile
+    uint64_t info[kInfo];
+    uint32_t valid[kInfo];                     // slices of a tile that were loaded, by tile
     uint32_t tmem_base;
     int32_t abort;
     float top[2][64], sum[2][64];              // a row's halves, exchanged
@@ -138,7 +136,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             mbar_init(&bars->p_full[i], 8);
             mbar_init(&bars->pv_done[i], 1);
         }
-        for (int i = 0; i < kValid; ++i) mbar_init(&bars->info[i], 1);
+        for (int i = 0; i < kInfo; ++i) mbar_init(&bars->info[i], 1);
         bars->abort = 0;
         fence_mbar_init();
         tc::prefetch_tmap(&tmap_q);
@@ -153,12 +151,13 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     griddep_launch();
 
     int64_t per;
-    Line line = find_stretch<kPairThreads>(p, group, blockIdx.x == 0, bars->scan, per);
+    Line line;
+    Part w;
+    const bool some = find_stretch<kPairThreads>(p, group, blockIdx.x == 0, bars->scan, line, w, per);
     tc::fence_before_sync();
     tc::cluster_sync();
     tc::fence_after_sync();
     const uint32_t tmem = bars->tmem_base;     // S of tile i: columns 32 (i mod 2) ..; O: 128 + 128 j ..
-    Part w;
 
     if (warp == 0) {
         // ------------------------------------------------------------ Q and K
@@ -166,9 +165,20 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int size = 1 << sl.log2_size;
         bool ok = true;
         uint32_t it = 0, q_n = 0;
-        for (int unit = 0; ok && next_part(p, line, w); ++unit) {
+        for (int unit = 0; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
+            auto load_q = [&] {
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive_expect_tx(&bars->q_full, 2 * L::kBlocks * L::kQBlock);
+                    const uint32_t bar = tc::cluster_addr(&bars->q_full, 0);
+                    for (int b = 0; b < L::kBlocks; ++b)
+                        tc::tma2_load_2d(smem + b * L::kQBlock, &tmap_q, b * 64, w.row + 64 * (int)rank, bar);
+                }
+                __syncwarp();
+                ++q_n;
+            };
             int32_t next = sl.fetch(w, table, w.t0);
+            if (unit == 0) load_q();
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const int32_t id = next;
                 next = sl.fetch(w, table, t + 1);
@@ -181,24 +191,17 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     break;
                 if (lane == 0) {
                     if (rank == 0) mbar_arrive_expect_tx(&bars->k_full[slot], __popc(mask) * size * L::kBlocks * 128);
-                    bars->valid[it % kValid] = mask;
-                    mbar_arrive(&bars->info[it % kValid]);
+                    bars->valid[it % kInfo] = mask;
+                    mbar_arrive(&bars->info[it % kInfo]);
                 }
                 __syncwarp();
                 const int tok = lane << sl.log2_size;
                 if (live && (uint32_t)(tok >> 5) == rank)
                     tc::tma2_load_4d(smem + L::kK + slot * L::kKBytes + ((tok & 31) >> 3) * (L::kBlocks * 1024),
                                      &tmap_k, 0, 0, 0, row >> 3, tc::cluster_addr(&bars->k_full[slot], 0));
-                if (t == w.t0) {  // Q behind the unit's first tile: it waits for the unit before
-                    if (unit > 0 && !(ok = wait_warp(&bars->q_empty, (unit - 1) & 1, bars, p.d_err))) break;
-                    if (lane == 0) {
-                        if (rank == 0) mbar_arrive_expect_tx(&bars->q_full, 2 * L::kBlocks * L::kQBlock);
-                        const uint32_t bar = tc::cluster_addr(&bars->q_full, 0);
-                        for (int b = 0; b < L::kBlocks; ++b)
-                            tc::tma2_load_2d(smem + b * L::kQBlock, &tmap_q, b * 64, w.row + 64 * (int)rank, bar);
-                    }
-                    __syncwarp();
-                    ++q_n;
+                if (t == w.t0 && unit > 0) {  // Q behind the unit's first tile: it waits for the unit before
+                    if (!(ok = wait_warp(&bars->q_empty, (unit - 1) & 1, bars, p.d_err))) break;
+                    load_q();
                 }
             }
         }
@@ -214,7 +217,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int size = 1 << sl.log2_size;
         bool ok = true;
         uint32_t it = 0;
-        while (ok && next_part(p, line, w)) {
+        for (int unit = 0; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
             int32_t next = sl.fetch(w, table, w.t0);
             for (int t = w.t0; t < w.t1; ++t, ++it) {
@@ -246,7 +249,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const uint64_t dk = tc::smem_desc_sw128(smem_u32(smem + L::kK), 16, L::kBlocks * 1024);
         uint32_t slot = 0, phase = 0, it = 0;
         bool ok = rank == 0;
-        for (int unit = 0; ok && __any_sync(0xffffffffu, next_part(p, line, w)); ++unit) {
+        for (int unit = 0; ok && __any_sync(0xffffffffu, unit == 0 ? some : next_part(p, line, w)); ++unit) {
             const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
             if (!(ok = wait_cluster(&bars->q_full, unit & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
@@ -277,7 +280,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const uint64_t dv = tc::smem_desc_sw128(smem_u32(smem + L::kV), 1024, NJ * 2048);
         uint32_t slot = 0, it = 0;
         bool ok = rank == 0;
-        for (int unit = 0; ok && __any_sync(0xffffffffu, next_part(p, line, w)); ++unit) {
+        for (int unit = 0; ok && __any_sync(0xffffffffu, unit == 0 ? some : next_part(p, line, w)); ++unit) {
             const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
             if (unit > 0 && !(ok = wait_cluster(&bars->o_free, (unit - 1) & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
@@ -315,7 +318,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // limit, so none may stay away)
         bool ok = true;
         int32_t chain_rows = 0, chain_row = 0, chain = 0;
-        for (int unit = 0; next_part(p, line, w); ++unit) {
+        for (int unit = 0; unit == 0 ? some : next_part(p, line, w); ++unit) {
             const int ur = r + 64 * (int)rank;         // row of the unit
             int lim = 0;                               // tokens that it sees
             if (ur < w.rows) lim = p.causal ? w.q.n - w.q.fresh + (w.token + ur) / p.heads + 1 : w.q.n;
@@ -324,11 +327,11 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             float m = -INFINITY, l = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const uint32_t b = it & 1;
-                ok &= wait_warp(&bars->info[it % kValid], (it / kValid) & 1, bars, p.d_err);
+                ok &= wait_warp(&bars->info[it % kInfo], (it / kInfo) & 1, bars, p.d_err);
                 ok &= wait_cluster(&bars->s_full[b], (it >> 1) & 1, bars, p.d_err);
                 tc::fence_after_sync();
                 const int pos = t * kTok;
-                const uint32_t valid = *(volatile uint32_t*)&bars->valid[it % kValid];
+                const uint32_t valid = *(volatile uint32_t*)&bars->valid[it % kInfo];
                 const bool whole = valid == all && pos + kTok <= ctx;
                 uint32_t s[32];
                 tc::tmem_ld32(tmem + 32 * b + lanes, s);
@@ -428,31 +431,61 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             }
             ok &= wait_cluster(&bars->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, bars, p.d_err);
             tc::fence_after_sync();
-#pragma unroll 1
-            for (int c = 0; c < NJ * 128; c += 32) {
-                uint32_t o[32];
-                tc::tmem_ld32(tmem + 128 + c + lanes, o);
-                tc::tmem_wait_ld();
-                const int dim = (c >> 7) * 256 + half * 128 + (c & 127);
-                if (ur < w.rows && cut) {
-                    float4* dst = reinterpret_cast<float4*>(p.parts + (slot * p.R + ur) * kDim + dim);
+            // a warp's 32 rows x 128 bytes at a time through its quarter of the P buffers
+            // (their products are done), so that stores fill whole lines: a lane's own row
+            // would be 32 pieces of 16 bytes a store
+            const uint32_t stage = smem_u32(smem + L::kP) + quarter * 4096;
+            const int base = 64 * (int)rank + (quarter & 1) * 32;  // unit row of the warp's first lane
+            auto spill = [&](int e, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                             ::"r"(stage + lane * 128 + ((e ^ (lane & 7)) << 4)), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+            };
+            auto drain = [&](char* dst, int64_t pitch) {
+                __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                             __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-                } else if (ur < w.rows) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)(w.row + ur) * kDim + dim);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[i] = pack_bf16(__uint_as_float(o[8 * e + 2 * i]) * inv,
-                                             __uint_as_float(o[8 * e + 2 * i + 1]) * inv);
-                        dst[e] = make_uint4(x[0], x[1], x[2], x[3]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 4 * i + (lane >> 3);
+                    uint4 x;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                 : "r"(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4)));
+                    if (base + row < w.rows)
+                        *reinterpret_cast<uint4*>(dst + row * pitch + (lane & 7) * 16) = x;
                 }
                 __syncwarp();
+            };
+            if (cut) {
+#pragma unroll 1
+                for (int c = 0; c < NJ * 128; c += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tmem + 128 + c + lanes, o);
+                    tc::tmem_wait_ld();
+                    const int dim = (c >> 7) * 256 + half * 128 + (c & 127);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) spill(e, o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    drain((char*)(p.parts + (slot * p.R + base) * kDim + dim), kDim * 4);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < NJ * 128; c += 64) {
+                    const int dim = (c >> 7) * 256 + half * 128 + (c & 127);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(tmem + 128 + c + 32 * g + lanes, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                x[i] = pack_bf16(__uint_as_float(o[8 * e + 2 * i]) * inv,
+                                                 __uint_as_float(o[8 * e + 2 * i + 1]) * inv);
+                            spill(4 * g + e, x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                    drain((char*)(p.out + (int64_t)(w.row + base) * kDim + dim), kDim * 2);
+                }
             }
             tc::fence_before_sync();
             __syncwarp();
