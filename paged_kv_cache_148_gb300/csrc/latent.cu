@@ -79,7 +79,8 @@ struct Bars {
     uint64_t s_full[2], p_full[2], pv_done[2];
     uint32_t tmem_base;
     int32_t abort;
-    uint64_t info[kInfo];
+    uint64_t info[kInfo], unit_info[kUnits];
+    int32_t unit_tiles[kUnits];
     uint32_t valid[kInfo];           // pages of a tile that were loaded, by tile
     float factor[64];                // rescaling factors of the rows
     float inv[2][64];                // one over the rows' sums, by unit mod 2
@@ -152,6 +153,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             mbar_init(&bars->pv_done[i], 1);
         }
         for (int i = 0; i < kInfo; ++i) mbar_init(&bars->info[i], 1);
+        for (int i = 0; i < kUnits; ++i) mbar_init(&bars->unit_info[i], 1);
         bars->abort = 0;
         fence_mbar_init();
         tc::prefetch_tmap(&tmap_q);
@@ -187,11 +189,20 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         bool ok = true;
         uint32_t part_n = 0, rope_n = 0, q_n = 0;    // loads issued so far
         uint32_t it = 0;
-        for (int unit = 0; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
+        auto tell = [&](int unit, int tiles) {
+            if (lane == 0) {
+                bars->unit_tiles[unit % kUnits] = tiles;
+                mbar_arrive(&bars->unit_info[unit % kUnits]);
+            }
+            __syncwarp();
+        };
+        int unit = 0;
+        for (; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
+            tell(unit, w.t1 - w.t0);
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
             auto fetch = [&](int t) -> int32_t {     // this lane's page of tile t; -1 past the end
                 const int64_t pos = (int64_t)t * kTok + lane * box;
-                if (lane >= pages || t >= w.t1 || pos >= w.limit) return INT32_MIN;
+                if (lane >= pages || t >= w.t1 || pos >= w.context) return INT32_MIN;
                 const int64_t e = pos >> p.log2_bp;
                 return e < p.max_blocks ? max(__ldg(table + e), -1) : p.num_blocks;
             };
@@ -206,6 +217,8 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             };
             int32_t next = fetch(w.t0);
             if (unit == 0) load_q();
+            if (lane == 0) ask_next_q(p, line, w, R, (kDim + p.rope_dim) * 2);
+            __syncwarp();
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const int32_t id = next;
                 next = fetch(t + 1);
@@ -251,6 +264,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 }
             }
         }
+        if (ok) tell(unit, 0);
         __syncwarp();
         if (!ok) {  // a wait ran out: no copy may still be on its way when the CTA ends
             for (uint32_t n = part_n - min(part_n, (uint32_t)L::kSlots); n < part_n; ++n)
@@ -269,9 +283,9 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const int rope_steps = p.rope_dim >> 4;
         uint32_t slot = 0, phase = 0, slot_r = 0, phase_r = 0, it = 0;
         bool ok = true;
-        for (int unit = 0; ok && __any_sync(0xffffffffu, unit == 0 ? some : next_part(p, line, w)); ++unit) {
-            const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
-            if (!(ok = wait_warp(&bars->q_full, unit & 1, bars, p.d_err))) break;
+        for (int unit = 0; ok && (ok = wait_warp(&bars->unit_info[unit % kUnits], (unit / kUnits) & 1, bars, p.d_err)); ++unit) {
+            const int n = __reduce_max_sync(0xffffffffu, *(volatile int32_t*)&bars->unit_tiles[unit % kUnits]);
+            if (n == 0 || !(ok = wait_warp(&bars->q_full, unit & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
                 // the softmax has read this buffer's last tile
                 if (it >= 2 && !(ok = wait_warp(&bars->p_full[it & 1], ((it >> 1) - 1) & 1, bars, p.d_err))) break;
@@ -315,8 +329,9 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const uint64_t dp = tc::smem_desc_sw128(tP, 16, 1024);
         uint32_t slot = 0, it = 0;
         bool ok = true;
-        for (int unit = 0; ok && __any_sync(0xffffffffu, unit == 0 ? some : next_part(p, line, w)); ++unit) {
-            const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
+        for (int unit = 0; ok && (ok = wait_warp(&bars->unit_info[unit % kUnits], (unit / kUnits) & 1, bars, p.d_err)); ++unit) {
+            const int n = __reduce_max_sync(0xffffffffu, *(volatile int32_t*)&bars->unit_tiles[unit % kUnits]);
+            if (n == 0) break;
             if (unit > 0 && !(ok = wait_warp(&bars->o_free, (unit - 1) & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
                 if (!(ok = wait_warp(&bars->p_full[it & 1], (it >> 1) & 1, bars, p.d_err))) break;
@@ -354,12 +369,8 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         bool ok = true;
         int32_t chain_rows = 0, chain_row = 0, chain = 0;
         for (int unit = 0; unit == 0 ? some : next_part(p, line, w); ++unit) {
-            int lim0 = 0, lim1 = 0;                    // tokens that the two rows see
-            if (r0 < w.rows) lim0 = p.causal ? w.q.n - w.q.fresh + (w.token + r0) / p.heads + 1 : w.q.n;
-            if (r1 < w.rows) lim1 = p.causal ? w.q.n - w.q.fresh + (w.token + r1) / p.heads + 1 : w.q.n;
-            lim0 = min(lim0, p.max_context);
-            lim1 = min(lim1, p.max_context);
-            const int ctx = min(w.q.n, p.max_context);
+            const int lim0 = w.seen(p, r0), lim1 = w.seen(p, r1);  // tokens that the two rows see
+            const int ctx = w.context;
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const int b = (int)(it & 1);
@@ -456,8 +467,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     // tokens that nobody wrote or loaded: their probability is zero, and
                     // so must their value be (zero times NaN is NaN)
                     const int tok = tid & 63;
-                    const int page_end = ((w.limit + (1 << log2_box) - 1) >> log2_box) << log2_box;
-                    if (pos + tok >= min(ctx, page_end) || !((valid >> (tok >> log2_box)) & 1)) {
+                    if (pos + tok >= ctx || !((valid >> (tok >> log2_box)) & 1)) {
                         for (int m = tid >> 6; m < 2 * PAIRS; m += 2) {
                             const uint32_t n = (uint32_t)(it * L::kParts + m / L::C);
                             const uint32_t at = tRing + (n % L::kSlots) * L::kPart + (tok >> 3) * (L::C * 1024) +
@@ -465,7 +475,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
-                                             ::"r"(at + c * 16), "r"(0) : "memory");
+                                             ::"r"(at + (((c + tok) & 7) << 4)), "r"(0) : "memory");
                         }
                     }
                 }
@@ -785,6 +795,7 @@ static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t he
     if (workspace == nullptr || workspace_bytes < sh.bytes || !aligned16(workspace))
         return PA_ERR_INVALID_ARG;
     Params p;
+    p.q = (const char*)q;
     p.num_blocks = pool->num_blocks;
     p.log2_bp = ilog2(pool->block_size);
     p.latent_dim = pool->latent_dim;

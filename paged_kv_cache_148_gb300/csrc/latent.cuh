@@ -19,8 +19,15 @@ constexpr int kSmemLimit = 232448;   // 227 KB
 // Rings of what the producer tells the softmax about a tile: it is at most kSlots + 2
 // tiles ahead of its slowest reader.
 constexpr int kInfo = 8;
+// And what it tells the issuers about a unit: its tiles, 0 behind the last.  The issuers
+// know no more of units: with the search for them in their loops the compiler loses
+// track of what is uniform in the warp, and an MMA with descriptors from general
+// registers takes 40 to 100 cycles to issue, against 24 to 64 to run.  The producer is
+// at most two units ahead of them (Q has one buffer).
+constexpr int kUnits = 4;
 
 struct Params {
+    const char* q;
     int32_t num_blocks, log2_bp, latent_dim, rope_dim;
     int32_t heads;
     const int32_t *starts, *lens, *tables;  // starts: null for one query a sequence
@@ -121,58 +128,52 @@ struct Part {
     int32_t row;          // first query row of the unit, over the whole call
     int32_t rows;         // its rows
     int32_t token;        // first row's index within the sequence's rows
-    int32_t limit;        // tokens that the unit's last row sees
+    int32_t ahead;        // tokens before the sequence's first new one
+    int32_t context;      // tokens of the sequence that may be seen
     int32_t t0, t1;       // tiles
     int32_t tiles;        // of the whole unit
     int64_t unit_at;      // the unit's place on the line
-    Seq q;
+
+    // tokens that row r of the unit sees
+    PA_DEVICE int32_t seen(const Params& p, int r) const {
+        if (r >= rows) return 0;
+        return p.causal ? min(ahead + (token + r) / p.heads + 1, context) : context;
+    }
 };
 
 struct Line {
     int64_t at, end;      // what is left of the stretch
-    int64_t seq_at;       // place of sequence s on the line
-    int32_t s;
+    int64_t unit_at;      // place of unit u of sequence s on the line
+    int32_t s, u;
+    Seq q;
 };
 
 // The next share of the stretch, skipping places that the line holds too many.
 PA_DEVICE bool next_part(const Params& p, Line& l, Part& w) {
-    while (l.at < l.end && l.s < p.seqs) {
-        const Seq q = read_seq(p, l.s, false);
-        const int64_t all = q.before(q.units);
-        if (l.at >= l.seq_at + all) {
-            l.seq_at += all;
-            ++l.s;
+    while (l.at < l.end) {
+        if (l.u >= l.q.units) {
+            if (++l.s >= p.seqs) return false;
+            l.q = read_seq(p, l.s, false);
+            l.u = 0;
             continue;
         }
-        int u = 0, hi = q.units - 1;       // last unit that begins at or before `at`
-        const int64_t off = l.at - l.seq_at;
-        while (u < hi) {
-            const int mid = (int)(((unsigned)u + hi + 1) >> 1);
-            if (q.before(mid) <= off) u = mid; else hi = mid - 1;
-        }
-        const int64_t begin = l.seq_at + q.before(u), stop = l.seq_at + q.before(u + 1);
+        const int u = l.u++;
+        const int64_t begin = l.unit_at;
+        l.unit_at = begin + l.q.first + (l.q.step == 0 ? 0 : l.q.more * (u / l.q.step));
+        if (l.at >= l.unit_at) continue;
         const int r0 = u * p.unit_rows;
-        const int all_rows = min(q.fresh, p.max_q) * p.heads;
-        const int rows = min(p.unit_rows, all_rows - r0);
-        int seen = q.n;
-        if (p.causal) seen = q.n - q.fresh + (r0 + rows - 1) / p.heads + 1;
-        seen = min(seen, p.max_context);
-        const int tiles = (seen + kTok - 1) / kTok;
-        const int t0 = (int)(l.at - begin);
-        const int t1 = (int)min((int64_t)tiles, l.end - begin);
-        l.at = min(stop, l.end);
-        if (t0 >= t1) continue;
         w.seq = l.s;
-        w.row = q.start * p.heads + r0;
-        w.rows = rows;
+        w.row = l.q.start * p.heads + r0;
+        w.rows = min(p.unit_rows, min(l.q.fresh, p.max_q) * p.heads - r0);
         w.token = r0;
-        w.limit = seen;
-        w.t0 = t0;
-        w.t1 = t1;
-        w.tiles = tiles;
+        w.ahead = l.q.n - l.q.fresh;
+        w.context = min(l.q.n, p.max_context);
+        w.tiles = (w.seen(p, w.rows - 1) + kTok - 1) / kTok;
+        w.t0 = (int)(l.at - begin);
+        w.t1 = (int)min((int64_t)w.tiles, l.end - begin);
         w.unit_at = begin;
-        w.q = q;
-        return true;
+        l.at = min(l.unit_at, l.end);
+        if (w.t0 < w.t1) return true;
     }
     return false;
 }
@@ -223,7 +224,20 @@ PA_DEVICE bool find_stretch(const Params& p, int group, bool report, Scan& sc, L
     ahead += upto - mine;
     if (line.at < line.end && ahead <= line.at && line.at < ahead + mine) {
         line.s = s0;
-        line.seq_at = ahead;
+        line.unit_at = ahead;
+        line.q = read_seq(p, s0, false);
+        for (int64_t all; line.at >= line.unit_at + (all = line.q.before(line.q.units));) {
+            line.unit_at += all;
+            line.q = read_seq(p, ++line.s, false);
+        }
+        const int64_t off = line.at - line.unit_at;
+        int u = 0, hi = line.q.units - 1;  // last unit that begins at or before `at`
+        while (u < hi) {
+            const int mid = (int)(((unsigned)u + hi + 1) >> 1);
+            if (line.q.before(mid) <= off) u = mid; else hi = mid - 1;
+        }
+        line.u = u;
+        line.unit_at += line.q.before(u);
         sc.some = next_part(p, line, part);
         sc.line = line;
         sc.part = part;
@@ -232,6 +246,15 @@ PA_DEVICE bool find_stretch(const Params& p, int group, bool report, Scan& sc, L
     line = sc.line;
     part = sc.part;
     return sc.some != 0;
+}
+
+// Asks for the rows behind this unit's, the next unit's queries, in L2: the stretch goes
+// on with them, and HBM's latency would stand between the two units.
+PA_DEVICE void ask_next_q(const Params& p, const Line& l, const Part& w, int rows, int row_bytes) {
+    const int64_t first = (int64_t)w.row + w.rows, left = (int64_t)p.total_q * p.heads - first;
+    if (l.at < l.end && left > 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                     ::"l"(p.q + first * row_bytes), "r"((uint32_t)min((int64_t)rows, left) * row_bytes) : "memory");
 }
 
 // Tiles of the pair kernel (latent_pair.cu): units of up to 128 rows, a CTA pair each.

@@ -48,7 +48,8 @@ struct PairBars {
     uint64_t q_full, q_empty, o_free;          // q_full, o_free, k_full, p_full: the leader's
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
     uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t info[kInfo];
+    uint64_t info[kInfo], unit_info[kUnits];
+    int32_t unit_tiles[kUnits];
     uint32_t valid[kInfo];                     // slices of a tile that were loaded, by tile
     uint32_t tmem_base;
     int32_t abort;
@@ -91,7 +92,7 @@ struct Slices {
 
     PA_DEVICE int32_t fetch(const Part& w, const int32_t* table, int t) const {
         const int64_t pos = (int64_t)t * kTok + (lane << log2_size);
-        if (lane >= (kTok >> log2_size) || t >= w.t1 || pos >= w.limit) return INT32_MIN;
+        if (lane >= (kTok >> log2_size) || t >= w.t1 || pos >= w.context) return INT32_MIN;
         const int64_t e = pos >> p.log2_bp;
         return e < p.max_blocks ? max(__ldg(table + e), -1) : p.num_blocks;
     }
@@ -137,6 +138,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             mbar_init(&bars->pv_done[i], 1);
         }
         for (int i = 0; i < kInfo; ++i) mbar_init(&bars->info[i], 1);
+        for (int i = 0; i < kUnits; ++i) mbar_init(&bars->unit_info[i], 1);
         bars->abort = 0;
         fence_mbar_init();
         tc::prefetch_tmap(&tmap_q);
@@ -165,7 +167,16 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int size = 1 << sl.log2_size;
         bool ok = true;
         uint32_t it = 0, q_n = 0;
-        for (int unit = 0; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
+        auto tell = [&](int unit, int tiles) {
+            if (lane == 0) {
+                bars->unit_tiles[unit % kUnits] = tiles;
+                mbar_arrive(&bars->unit_info[unit % kUnits]);
+            }
+            __syncwarp();
+        };
+        int unit = 0;
+        for (; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
+            tell(unit, w.t1 - w.t0);
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
             auto load_q = [&] {
                 if (lane == 0) {
@@ -179,6 +190,8 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             };
             int32_t next = sl.fetch(w, table, w.t0);
             if (unit == 0) load_q();
+            if (lane == 0 && rank == 0) ask_next_q(p, line, w, 128, L::kBlocks * 128);
+            __syncwarp();
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const int32_t id = next;
                 next = sl.fetch(w, table, t + 1);
@@ -205,6 +218,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 }
             }
         }
+        if (ok) tell(unit, 0);
         __syncwarp();
         if (!ok && rank == 0) {  // a wait ran out: no copy may still be on its way when the CTAs end
             for (uint32_t n = it - min(it, (uint32_t)L::kSlots); n < it; ++n)
@@ -249,9 +263,9 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const uint64_t dk = tc::smem_desc_sw128(smem_u32(smem + L::kK), 16, L::kBlocks * 1024);
         uint32_t slot = 0, phase = 0, it = 0;
         bool ok = rank == 0;
-        for (int unit = 0; ok && __any_sync(0xffffffffu, unit == 0 ? some : next_part(p, line, w)); ++unit) {
-            const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
-            if (!(ok = wait_cluster(&bars->q_full, unit & 1, bars, p.d_err))) break;
+        for (int unit = 0; ok && (ok = wait_warp(&bars->unit_info[unit % kUnits], (unit / kUnits) & 1, bars, p.d_err)); ++unit) {
+            const int n = __reduce_max_sync(0xffffffffu, *(volatile int32_t*)&bars->unit_tiles[unit % kUnits]);
+            if (n == 0 || !(ok = wait_cluster(&bars->q_full, unit & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
                 // the softmax of both CTAs has read this buffer's last tile
                 if (it >= 2 && !(ok = wait_cluster(&bars->p_full[it & 1], ((it >> 1) - 1) & 1, bars, p.d_err))) break;
@@ -280,8 +294,9 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const uint64_t dv = tc::smem_desc_sw128(smem_u32(smem + L::kV), 1024, NJ * 2048);
         uint32_t slot = 0, it = 0;
         bool ok = rank == 0;
-        for (int unit = 0; ok && __any_sync(0xffffffffu, unit == 0 ? some : next_part(p, line, w)); ++unit) {
-            const int n = __reduce_max_sync(0xffffffffu, w.t1 - w.t0);
+        for (int unit = 0; ok && (ok = wait_warp(&bars->unit_info[unit % kUnits], (unit / kUnits) & 1, bars, p.d_err)); ++unit) {
+            const int n = __reduce_max_sync(0xffffffffu, *(volatile int32_t*)&bars->unit_tiles[unit % kUnits]);
+            if (n == 0) break;
             if (unit > 0 && !(ok = wait_cluster(&bars->o_free, (unit - 1) & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
                 if (!(ok = wait_cluster(&bars->p_full[it & 1], (it >> 1) & 1, bars, p.d_err))) break;
@@ -320,10 +335,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         int32_t chain_rows = 0, chain_row = 0, chain = 0;
         for (int unit = 0; unit == 0 ? some : next_part(p, line, w); ++unit) {
             const int ur = r + 64 * (int)rank;         // row of the unit
-            int lim = 0;                               // tokens that it sees
-            if (ur < w.rows) lim = p.causal ? w.q.n - w.q.fresh + (w.token + ur) / p.heads + 1 : w.q.n;
-            lim = min(lim, p.max_context);
-            const int ctx = min(w.q.n, p.max_context);
+            const int lim = w.seen(p, ur), ctx = w.context;
             float m = -INFINITY, l = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const uint32_t b = it & 1;
@@ -408,7 +420,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
-                                             ::"r"(at + i * 1024 + c * 16), "r"(0) : "memory");
+                                             ::"r"(at + i * 1024 + (((c + tok) & 7) << 4)), "r"(0) : "memory");
                     }
                 }
                 fence_proxy_async_smem();
