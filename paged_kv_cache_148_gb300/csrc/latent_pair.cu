@@ -58,33 +58,6 @@ struct PairBars {
 };
 static_assert(sizeof(PairBars) <= kPairBars, "barrier area");
 
-PA_DEVICE bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return ok != 0;
-}
-
-// wait_warp for barriers that the other CTA's threads or loads arrive on.
-PA_DEVICE bool wait_cluster(uint64_t* bar, uint32_t parity, PairBars* b, int32_t* d_err) {
-    bool ok = try_wait_cluster(bar, parity);
-    if (!ok) {
-        const uint64_t t0 = global_timer_ns();
-        while (!(ok = try_wait_cluster(bar, parity))) {
-            if (*(volatile int32_t*)&b->abort) break;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-                set_error(d_err, PA_ERR_TIMEOUT);
-                *(volatile int32_t*)&b->abort = 1;
-                break;
-            }
-        }
-    }
-    return __all_sync(0xffffffffu, ok);
-}
-
 // One lane's slice of a tile: its page's row in the pool.
 struct Slices {
     const Params& p;
@@ -265,11 +238,11 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         bool ok = rank == 0;
         for (int unit = 0; ok && (ok = wait_warp(&bars->unit_info[unit % kUnits], (unit / kUnits) & 1, bars, p.d_err)); ++unit) {
             const int n = __reduce_max_sync(0xffffffffu, *(volatile int32_t*)&bars->unit_tiles[unit % kUnits]);
-            if (n == 0 || !(ok = wait_cluster(&bars->q_full, unit & 1, bars, p.d_err))) break;
+            if (n == 0 || !(ok = wait_warp(&bars->q_full, unit & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
                 // the softmax of both CTAs has read this buffer's last tile
-                if (it >= 2 && !(ok = wait_cluster(&bars->p_full[it & 1], ((it >> 1) - 1) & 1, bars, p.d_err))) break;
-                if (!(ok = wait_cluster(&bars->k_full[slot], phase, bars, p.d_err))) break;
+                if (it >= 2 && !(ok = wait_warp(&bars->p_full[it & 1], ((it >> 1) - 1) & 1, bars, p.d_err))) break;
+                if (!(ok = wait_warp(&bars->k_full[slot], phase, bars, p.d_err))) break;
                 tc::fence_after_sync();
                 const uint32_t d = tmem + 32u * (it & 1);
                 const uint64_t b = dk + (uint64_t)(slot * (L::kKBytes >> 4));
@@ -297,9 +270,9 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         for (int unit = 0; ok && (ok = wait_warp(&bars->unit_info[unit % kUnits], (unit / kUnits) & 1, bars, p.d_err)); ++unit) {
             const int n = __reduce_max_sync(0xffffffffu, *(volatile int32_t*)&bars->unit_tiles[unit % kUnits]);
             if (n == 0) break;
-            if (unit > 0 && !(ok = wait_cluster(&bars->o_free, (unit - 1) & 1, bars, p.d_err))) break;
+            if (unit > 0 && !(ok = wait_warp(&bars->o_free, (unit - 1) & 1, bars, p.d_err))) break;
             for (int t = 0; t < n; ++t, ++it) {
-                if (!(ok = wait_cluster(&bars->p_full[it & 1], (it >> 1) & 1, bars, p.d_err))) break;
+                if (!(ok = wait_warp(&bars->p_full[it & 1], (it >> 1) & 1, bars, p.d_err))) break;
                 tc::fence_after_sync();
                 const uint64_t a = dp + (uint64_t)((it & 1) * (L::kPBytes >> 4));
                 const uint64_t b = dv + (uint64_t)(slot * (L::kVBytes >> 4));
@@ -340,7 +313,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const uint32_t b = it & 1;
                 ok &= wait_warp(&bars->info[it % kInfo], (it / kInfo) & 1, bars, p.d_err);
-                ok &= wait_cluster(&bars->s_full[b], (it >> 1) & 1, bars, p.d_err);
+                ok &= wait_warp(&bars->s_full[b], (it >> 1) & 1, bars, p.d_err);
                 tc::fence_after_sync();
                 const int pos = t * kTok;
                 const uint32_t valid = *(volatile uint32_t*)&bars->valid[it % kInfo];
@@ -374,7 +347,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     m = up;
                     l *= f;
                     if (__any_sync(0xffffffffu, f != 1.f)) {
-                        ok &= wait_cluster(&bars->pv_done[b ^ 1], ((it - 1) >> 1) & 1, bars, p.d_err);
+                        ok &= wait_warp(&bars->pv_done[b ^ 1], ((it - 1) >> 1) & 1, bars, p.d_err);
                         tc::fence_after_sync();
 #pragma unroll 1
                         for (int c = 0; c < NJ * 128; c += 32) {
@@ -402,7 +375,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 }
                 l += ls[0] + ls[1];
                 // P's buffer was last read by the product two tiles ago
-                if (it >= 2) ok &= wait_cluster(&bars->pv_done[b], ((it >> 1) - 1) & 1, bars, p.d_err);
+                if (it >= 2) ok &= wait_warp(&bars->pv_done[b], ((it >> 1) - 1) & 1, bars, p.d_err);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
@@ -441,7 +414,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 chain_row = w.row;
                 chain_rows = w.rows;
             }
-            ok &= wait_cluster(&bars->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, bars, p.d_err);
+            ok &= wait_warp(&bars->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, bars, p.d_err);
             tc::fence_after_sync();
             // a warp's 32 rows x 128 bytes at a time through its quarter of the P buffers
             // (their products are done), so that stores fill whole lines: a lane's own row
