@@ -172,6 +172,8 @@ extern "C" pa_status pa_write_latent(const pa_latent_pool* pool, const pa_rope* 
     p.q = (uint16_t*)q;
     p.rows = (uint16_t*)pool->rows;
     p.d_err = d_err;
+    // tokens a CTA (8192 tokens of 32 heads: 22.7, 20.5, 18.6 us with 1, 2, 4); small batches
+    // need the CTAs
     const int per = num_tokens >= 4 * device_sm_count() ? 4 : 1;
     cudaError_t e = launch_pdl(latent_write_kernel, dim3((unsigned)((num_tokens + per - 1) / per)),
                                dim3(kLatentWriteThreads),
