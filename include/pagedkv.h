@@ -521,7 +521,8 @@ pa_status pa_copy_latent_blocks(const pa_latent_pool* pool, const int32_t* src, 
  *                 contexts that are split; calls that may overlap need one each.
  * block_tables, context_lens (0 leaves out[s] untouched), max_context, and
  * errors as pa_decode; a sequence whose every page is outside the pool gets
- * zeros.  Rows past a context's end are never used, whatever they hold.
+ * zeros.  Rows past a context's end are never used, whatever they hold; rows
+ * within it are finite.
  * Implemented: latent_dim 128, 256, 384 or 512, rope_dim 16, 32, 48 or 64,
  * block size a power of two in [8, 128], num_q_heads <= 128, at most 65535
  * sequences, num_blocks * block_size < 2^31; others UNSUPPORTED.
@@ -543,7 +544,9 @@ pa_status pa_decode_latent(const pa_latent_pool* pool, const void* q, int32_t nu
  * cached part, drafted tokens to be checked): sequence s has the queries
  * q[cu_seqlens_q[s] .. cu_seqlens_q[s+1]), whose rows are already written; new
  * token i is at position context_lens[s] - n_new + i and sees positions 0 to
- * its own (causal != 0) or all context_lens[s].
+ * its own (causal != 0) or all context_lens[s].  (A row that is not finite
+ * reaches the queries that see it and may reach others of the same 128 query
+ * rows before it: their weight for it is zero, and zero times infinity is not.)
  *   q:    device bf16 [total_q][num_q_heads][latent_dim + rope_dim].
  *   out:  device bf16 [total_q][num_q_heads][latent_dim].
  * Sequences with no new token are skipped, and rows of q behind the last

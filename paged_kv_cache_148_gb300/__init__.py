@@ -905,8 +905,8 @@ def decode_latent(pool: LatentPool, q: torch.Tensor, block_tables: torch.Tensor,
     if T != B:
         raise ValueError("q must hold one token a sequence: %d, got %d" % (B, T))
     max_context = int(max_context)
-    need = _bytes_of(pool, decode_latent_workspace_bytes, B, H, max_context)
     with _On(pool.device, pool._index, stream) as on:
+        need = _bytes_of(pool, decode_latent_workspace_bytes, B, H, max_context)
         if out is None:
             out = on.made(torch.empty((T, H, pool.latent_dim), dtype=pool.dtype, device=pool.device))
         have = 0 if workspace is None else workspace.nbytes
@@ -931,8 +931,8 @@ def prefill_latent(pool: LatentPool, q: torch.Tensor, cu_seqlens_q: torch.Tensor
     T, H, B, width = _need_latent_q(pool, q, block_tables, context_lens, out, d_err, workspace)
     _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, pool.device, pool._index, (B + 1,))
     max_q_len, max_context = int(max_q_len), int(max_context)
-    need = _bytes_of(pool, prefill_latent_workspace_bytes, B, H, T, max_q_len, max_context)
     with _On(pool.device, pool._index, stream) as on:
+        need = _bytes_of(pool, prefill_latent_workspace_bytes, B, H, T, max_q_len, max_context)
         if out is None:
             out = on.made(torch.empty((T, H, pool.latent_dim), dtype=pool.dtype, device=pool.device))
         have = 0 if workspace is None else workspace.nbytes

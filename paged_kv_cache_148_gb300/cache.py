@@ -75,10 +75,11 @@ class PagedCache:
         """Append tokens whose q and k still need their positions; returns the rotated q."""
         first = self.lengths[sid]
         slots, cows = self.reserve(sid, int(k.shape[0]))
-        self.commit([], None, None, cows, d_err, stream)
-        positions = torch.arange(first, self.lengths[sid], device=self.device)
-        return rope_write_kv(self.pool, q, k, v, positions, torch.from_numpy(slots).to(self.device), rope,
-                             d_err=d_err, stream=stream)
+        with torch.cuda.stream(stream):  # made where they are used
+            self.commit([], None, None, cows, d_err, stream)
+            positions = torch.arange(first, self.lengths[sid], device=self.device)
+            return rope_write_kv(self.pool, q, k, v, positions, torch.from_numpy(slots).to(self.device),
+                                 rope, d_err=d_err, stream=stream)
 
     # ---------------------------------------------------------------- metadata
     def block_tables(self, sids: Optional[Sequence[int]] = None, width: Optional[int] = None):
@@ -107,14 +108,15 @@ class PagedLatentCache(PagedCache):
     def commit(self, slots, latent: torch.Tensor, k_rope: torch.Tensor, positions: torch.Tensor,
                rope: Rope, cows=(), q_rope=None, q=None, d_err=None, stream=None):
         """Copy-on-write copies (if any), then the write of the latent rows and of q's rotary part."""
-        if len(cows):
-            src = torch.tensor([a for a, _ in cows], dtype=torch.int32).to(self.device)
-            dst = torch.tensor([b for _, b in cows], dtype=torch.int32).to(self.device)
-            copy_latent_blocks(self.pool, src, dst, d_err=d_err, stream=stream)
-        if len(slots):
-            sm = slots if isinstance(slots, torch.Tensor) else torch.from_numpy(np.asarray(slots, np.int64))
-            write_latent(self.pool, latent, k_rope, positions, sm.to(self.device), rope,
-                         q_rope=q_rope, q=q, d_err=d_err, stream=stream)
+        with torch.cuda.stream(stream):  # the ids are made where they are used
+            if len(cows):
+                src = torch.tensor([a for a, _ in cows], dtype=torch.int32).to(self.device)
+                dst = torch.tensor([b for _, b in cows], dtype=torch.int32).to(self.device)
+                copy_latent_blocks(self.pool, src, dst, d_err=d_err, stream=stream)
+            if len(slots):
+                sm = slots if isinstance(slots, torch.Tensor) else torch.from_numpy(np.asarray(slots, np.int64))
+                write_latent(self.pool, latent, k_rope, positions, sm.to(self.device), rope,
+                             q_rope=q_rope, q=q, d_err=d_err, stream=stream)
 
     def append(self, sid: int, latent: torch.Tensor, k_rope: torch.Tensor, positions: torch.Tensor,
                rope: Rope, q_rope=None, q=None, d_err=None, stream=None):

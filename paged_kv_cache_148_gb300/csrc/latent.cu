@@ -370,7 +370,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         int32_t chain_rows = 0, chain_row = 0, chain = 0;
         for (int unit = 0; unit == 0 ? some : next_part(p, line, w); ++unit) {
             const int lim0 = w.seen(p, r0), lim1 = w.seen(p, r1);  // tokens that the two rows see
-            const int ctx = w.context;
+            const int ctx = w.seen(p, w.rows - 1);                 // and the unit's last row
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const int b = (int)(it & 1);
@@ -464,8 +464,9 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     }
                 }
                 if (!whole) {
-                    // tokens that nobody wrote or loaded: their probability is zero, and
-                    // so must their value be (zero times NaN is NaN)
+                    // tokens behind the unit's last row, which nobody may have written, and those
+                    // that were not loaded: their probability is zero, and so must their value
+                    // be (zero times NaN is NaN)
                     const int tok = tid & 63;
                     if (pos + tok >= ctx || !((valid >> (tok >> log2_box)) & 1)) {
                         for (int m = tid >> 6; m < 2 * PAIRS; m += 2) {

@@ -91,8 +91,6 @@ struct Seq {
     }
 };
 
-
-
 PA_DEVICE Seq read_seq(const Params& p, int s, bool report) {
     Seq q;
     q.units = q.first = q.step = q.more = 0;

@@ -308,7 +308,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         int32_t chain_rows = 0, chain_row = 0, chain = 0;
         for (int unit = 0; unit == 0 ? some : next_part(p, line, w); ++unit) {
             const int ur = r + 64 * (int)rank;         // row of the unit
-            const int lim = w.seen(p, ur), ctx = w.context;
+            const int lim = w.seen(p, ur), ctx = w.seen(p, w.rows - 1);  // tokens that this row sees, and the last
             float m = -INFINITY, l = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 const uint32_t b = it & 1;
@@ -383,8 +383,9 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                  "r"(pk[4 * i + 1]), "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3]) : "memory");
                 ok &= wait_warp(&bars->v_full[it % L::kSlots], (it / L::kSlots) & 1, bars, p.d_err);
                 if (!whole) {
-                    // tokens that nobody wrote or loaded: their probability is zero, and
-                    // so must their value be (zero times NaN is NaN)
+                    // tokens behind the unit's last row, which nobody may have written, and those
+                    // that were not loaded: their probability is zero, and so must their value
+                    // be (zero times NaN is NaN)
                     const int tok = tid & 63;
                     if (pos + tok >= ctx || !((valid >> (tok >> log2_size)) & 1)) {
                         const uint32_t at = smem_u32(smem + L::kV) + (it % L::kSlots) * L::kVBytes +

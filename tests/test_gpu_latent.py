@@ -377,3 +377,131 @@ def test_decoding_through_the_cache():
     d = pkv.decode_latent(cache.pool, q[[4, 6]].contiguous(), tables, lens, 64, 0.1)
     torch.cuda.synchronize()
     assert np.abs(_f64(d) - got[[4, 6]]).max() <= 2.0 ** -6 * np.abs(got).max()
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_pages_past_four_gigabytes(heads):
+    """Pages whose bytes lie past 2^32: every page at the end of a pool of 5.3 GB."""
+    pool = pkv.LatentPool(72000, 64, 512, 64)
+    assert pool.rows.numel() * 2 > 1 << 32
+    n, rope = 500, pkv.Rope(64)
+    ids = torch.arange(pool.num_blocks - 8, pool.num_blocks, dtype=torch.int32, device="cuda").flip(0)
+    j = torch.arange(n, device="cuda")
+    slots = ids.long()[j // 64] * 64 + j % 64
+    g = torch.Generator().manual_seed(heads)
+    draw = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    lat, kr, q = draw(n, 512), draw(n, 64), draw(1, heads, 576)
+    pos = torch.zeros(n, dtype=torch.int64, device="cuda")
+    pkv.write_latent(pool, lat, kr, pos, slots, rope)
+    # the last page moves to the front of the pool and back
+    src, dst = ids[7:].contiguous(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.copy_latent_blocks(pool, src, dst)
+    pool.rows[ids[7].item()] = float("nan")
+    pkv.copy_latent_blocks(pool, dst, src)
+    out = pkv.decode_latent(pool, q, ids[None].contiguous(), torch.tensor([n], dtype=torch.int32).cuda(), n, 0.07)
+    torch.cuda.synchronize()
+    ref, bound = orc.attend(_f64(q[0]), np.concatenate([_f64(lat), _f64(kr)], 1), 0.07, 512, [n] * heads)
+    assert (np.abs(_f64(out[0]) - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_two_calls_at_once(heads):
+    """Two streams, a workspace each, many times over: the calls do not meet."""
+    a, b = Batch([2000, 77, 900], heads, bp=16, seed=20), Batch([64, 1500], heads, bp=64, seed=21)
+    want_a, want_b = a.decode(), b.decode()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got.append((a.decode(stream=sa), b.decode(stream=sb)))
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert torch.equal(x, want_a) and torch.equal(y, want_b)
+    a.check(want_a, *a.reference(decode=True))
+
+
+@pytest.mark.parametrize("heads", [64, 128])
+def test_graphs_of_both_kernels(heads):
+    """A captured chunk and a captured step share one workspace, replayed in turn."""
+    b = Batch([700, 90, 1300], heads, bp=16, new=[40, 1, 65], seed=22)
+    d = Batch([700, 90, 1300], heads, bp=16, seed=22)
+    need = max(pkv.prefill_latent_workspace_bytes(b.pool, 3, heads, 106, 65, 1300),
+               pkv.decode_latent_workspace_bytes(d.pool, 3, heads, 1300))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want_p, want_d = b.prefill(workspace=ws), d.decode(workspace=ws)
+    torch.cuda.synchronize()
+    graphs = []
+    for call in (lambda: b.prefill(workspace=ws), lambda: d.decode(workspace=ws)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call()
+        graphs.append((g, out))
+    for _ in range(3):
+        for g, out in graphs:
+            out.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(graphs[0][1], want_p) and torch.equal(graphs[1][1], want_d)
+    b.check(want_p, *b.reference(tokens=[0, 39, 64]))
+
+
+def test_the_same_page_twice():
+    """A table may name a page twice, and two sequences the same pages."""
+    b = Batch([128, 128], 16, bp=64, seed=23)
+    b.tables.copy_(torch.tensor([[b.table_host[0, 0]] * 2, [b.table_host[0, 0]] * 2], dtype=torch.int32))
+    out = b.decode()
+    assert b.code() == 0
+    twice = np.concatenate([b.slots[0][:64]] * 2)
+    b.slots = [twice, twice]
+    b.check(out, *b.reference(decode=True))
+
+
+def test_later_rows_that_are_not_finite_stay_out():
+    """Rows behind a unit's last query, written or not, do not reach it."""
+    b = Batch([300], 128, bp=16, new=[2], seed=24)
+    flat = b.pool.rows.view(-1, b.pool.width)
+    flat[int(b.slots[0][299])] = float("inf")
+    out = b.prefill()            # 128 rows a unit: the first token alone
+    assert b.code() == 0
+    b.check(out, *b.reference(tokens=[0]))
+    assert not torch.isfinite(out[1]).all()
+
+
+def test_negative_scale():
+    b = Batch([300, 9], 16, bp=16, seed=25)
+    out = b.decode(scale=-0.05)
+    assert b.code() == 0
+    b.check(out, *b.reference(decode=True, scale=-0.05))
+
+
+def test_rotated_append_through_the_cache():
+    """Positions, copy on write and attention of an ordinary cache, as a server runs them."""
+    from paged_kv_cache_148_gb300.cache import PagedCache
+    cache = PagedCache(64, 16, 2, 128)
+    plain = PagedCache(64, 16, 2, 128)
+    rope = pkv.Rope(128)
+    g = torch.Generator().manual_seed(26)
+    draw = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    a, pa = cache.add_sequence(), plain.add_sequence()
+    f, m = orc.frequencies(128)
+    tails = []
+    side = torch.cuda.Stream()
+    for step, n in enumerate((21, 1, 5)):
+        if step == 1:
+            a, pa = cache.fork(a), plain.fork(pa)
+        first = cache.lengths[a]
+        q, k, v = draw(n, 8, 128), draw(n, 2, 128), draw(n, 2, 128)
+        side.wait_stream(torch.cuda.current_stream())
+        out = cache.append_rotated(a, q, k, v, rope, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        pos = np.arange(first, first + n)
+        rk, _ = orc.rotate(_f64(k), pos, f, "half", m)
+        plain.append(pa, torch.from_numpy(rk).to(torch.bfloat16), v)
+        ref, off = orc.rotate(_f64(q), pos, f, "half", m)
+        assert (np.abs(_f64(out) - ref) <= off + orc.BF16 * (np.abs(ref) + off)).all()
+        tails.append(out[-1:])
+    o = [pkv.decode(c.pool, tails[-1], c.block_tables([s]), c.context_lens([s]), 64, 0.09)
+         for c, s in ((cache, a), (plain, pa))]
+    torch.cuda.synchronize()
+    # keys differ by the last bit of bf16 at most where the two roundings disagree
+    assert (o[0] - o[1]).abs().max().item() <= 2.0 ** -7 * o[1].abs().max().item()
