@@ -135,30 +135,31 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     constexpr int kDim = PAIRS * 128;
     const int group = blockIdx.x;
 
-    if (threadIdx.x == 0) {
-        mbar_init(&bars->q_full, 1);
-        mbar_init(&bars->q_empty, 1);
-        mbar_init(&bars->o_free, 128);
-        for (int i = 0; i < kMaxParts; ++i) {
-            mbar_init(&bars->part_full[i], 1);
-            mbar_init(&bars->part_empty[i], 1);
+    if (warp == 0) {
+        if (lane < kMaxParts) {
+            mbar_init(&bars->part_full[lane], 1);
+            mbar_init(&bars->part_empty[lane], 1);
         }
-        for (int i = 0; i < kMaxRope; ++i) {
-            mbar_init(&bars->rope_full[i], 1);
-            mbar_init(&bars->rope_empty[i], 1);
+        if (lane < kInfo) mbar_init(&bars->info[lane], 1);
+        if (lane < kUnits) mbar_init(&bars->unit_info[lane], 1);
+        if (lane < 2) {
+            mbar_init(&bars->rope_full[lane], 1);
+            mbar_init(&bars->rope_empty[lane], 1);
+            mbar_init(&bars->s_full[lane], 1);
+            mbar_init(&bars->p_full[lane], 128);
+            mbar_init(&bars->pv_done[lane], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_full[i], 128);
-            mbar_init(&bars->pv_done[i], 1);
+        if (lane == 0) {
+            mbar_init(&bars->q_full, 1);
+            mbar_init(&bars->q_empty, 1);
+            mbar_init(&bars->o_free, 128);
+            bars->abort = 0;
+            tc::prefetch_tmap(&tmap_q);
+            tc::prefetch_tmap(&tmap_rows);
+            tc::prefetch_tmap(&tmap_rope);
         }
-        for (int i = 0; i < kInfo; ++i) mbar_init(&bars->info[i], 1);
-        for (int i = 0; i < kUnits; ++i) mbar_init(&bars->unit_info[i], 1);
-        bars->abort = 0;
         fence_mbar_init();
-        tc::prefetch_tmap(&tmap_q);
-        tc::prefetch_tmap(&tmap_rows);
-        tc::prefetch_tmap(&tmap_rope);
+        __syncwarp();
     }
     if (warp == 1) {
         tc::tmem_alloc(&bars->tmem_base, 512);
@@ -167,10 +168,7 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     griddep_wait();
     griddep_launch();
 
-    int64_t per;
-    Line line;
-    Part w;
-    const bool some = find_stretch<kThreads>(p, group, blockIdx.x == 0, bars->scan, line, w, per);
+    find_stretch<kThreads>(p, group, blockIdx.x == 0, bars->scan);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -196,6 +194,9 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             }
             __syncwarp();
         };
+        Line line = bars->scan.line;
+        Part w = bars->scan.part;
+        const bool some = bars->scan.some;
         int unit = 0;
         for (; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
             tell(unit, w.t1 - w.t0);
@@ -368,6 +369,10 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         // limit, so none may stay away)
         bool ok = true;
         int32_t chain_rows = 0, chain_row = 0, chain = 0;
+        Line line = bars->scan.line;
+        Part w = bars->scan.part;
+        const bool some = bars->scan.some;
+        const int64_t per = bars->scan.per;
         for (int unit = 0; unit == 0 ? some : next_part(p, line, w); ++unit) {
             const int lim0 = w.seen(p, r0), lim1 = w.seen(p, r1);  // tokens that the two rows see
             const int ctx = w.seen(p, w.rows - 1);                 // and the unit's last row
@@ -817,6 +822,11 @@ static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t he
     // unit_rows / heads tokens more a unit, 64 tokens a tile: a tile more every `step` units
     p.step = sh.unit_rows > 64 && heads > 1 ? heads / 2 : heads;
     p.more = sh.unit_rows > 64 && heads == 1 ? 2 : 1;
+    p.unit_shift = is_pow2(sh.unit_rows) && sh.unit_rows >= 64 ? ilog2(sh.unit_rows) : 0;
+    p.slack = (sh.unit_rows - 1) / heads;
+    p.unit_tokens = sh.unit_rows / heads;
+    p.unit_rest = sh.unit_rows % heads;
+    p.per_head = (65536u + heads - 1) / heads;
     p.groups = sh.groups;
     p.min_tiles = 2;
     p.out = (uint16_t*)out;

@@ -34,8 +34,12 @@ struct Params {
     int32_t max_blocks, seqs, max_q, total_q, max_context, causal;
     float scale_log2;
     int32_t unit_rows;               // rows of a unit
+    int32_t unit_shift;              // its logarithm where a sequence may have more than two units
     int32_t R;                       // unit_rows rounded up to 16
     int32_t step, more;              // causal: tiles that the line adds from unit to unit
+    int32_t slack;                   // causal: tokens, (unit_rows - 1) / heads
+    int32_t unit_tokens, unit_rest;  // unit_rows / heads and its remainder
+    uint32_t per_head;               // 65536 / heads, rounded up: x / heads for x < 256
     int32_t groups;                  // stretches
     int32_t min_tiles;               // least tiles a stretch
     uint16_t* out;
@@ -80,43 +84,46 @@ PA_DEVICE bool named_any(int id, bool x) {
 // tokens a unit; the line gives it first + more * (u / step) (host: step and more
 // from unit_rows and heads), at least as many and with a sum in closed form, so
 // that a stretch finds its place without walking the units.
+//
+// All of this runs once a launch with a cold instruction cache, some ten cycles an
+// instruction, so it is kept short: no division but in the search for a stretch's
+// first unit, steps from unit to unit by counters.
 struct Seq {
     int32_t start, fresh, n;   // first query token; query tokens; context
-    int32_t units, first, step, more;  // tiles of unit u: first + more * (u / step); step 0: first
+    int32_t units, first;      // tiles of unit u: first, with a mask + more * (u / step)
 
-    PA_DEVICE int64_t before(int u) const {
-        if (step == 0) return (int64_t)u * first;
-        const int64_t k = u / step;
-        return (int64_t)u * first + more * (step * (k * (k - 1) / 2) + k * (u - k * step));
+    PA_DEVICE int64_t before(const Params& p, int u) const {
+        const int64_t flat = (int64_t)u * first;
+        if (!p.causal || u <= p.step) return flat;
+        const int64_t k = u / p.step;
+        return flat + p.more * (p.step * (k * (k - 1) / 2) + k * (u - k * p.step));
     }
 };
 
 PA_DEVICE Seq read_seq(const Params& p, int s, bool report) {
     Seq q;
-    q.units = q.first = q.step = q.more = 0;
-    q.start = p.starts ? __ldg(p.starts + s) : s;
-    q.fresh = p.starts ? __ldg(p.starts + s + 1) - q.start : 1;
+    q.units = q.first = 0;
+    q.start = s;
+    q.fresh = 1;
     q.n = __ldg(p.lens + s);
-    if (p.starts && (q.start < 0 || q.fresh < 0 || q.fresh > p.total_q - q.start)) {
-        if (report) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
-        return q;
+    if (p.starts) {
+        q.start = __ldg(p.starts + s);
+        q.fresh = __ldg(p.starts + s + 1) - q.start;
+        if (q.start < 0 || q.fresh < 0 || q.fresh > p.total_q - q.start) {
+            if (report) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
+            return q;
+        }
+        if (q.fresh > 0 && q.n < q.fresh) {
+            if (report) set_error(p.d_err, PA_ERR_INVALID_ARG);
+            return q;
+        }
     }
-    if (q.fresh == 0 || (!p.starts && q.n <= 0)) return q;
-    if (q.n < q.fresh) {
-        if (report) set_error(p.d_err, PA_ERR_INVALID_ARG);
-        return q;
-    }
+    if (q.fresh == 0 || q.n <= 0) return q;
     if (report && (q.n > p.max_context || q.fresh > p.max_q)) set_error(p.d_err, PA_ERR_OUT_OF_RANGE);
-    const int64_t rows = (int64_t)min(q.fresh, p.max_q) * p.heads;
-    q.units = (int)((rows + p.unit_rows - 1) / p.unit_rows);
-    if (p.causal) {
-        const int64_t base = q.n - q.fresh;
-        q.first = (int)((base + 2 + (p.unit_rows - 1) / p.heads + kTok - 1) / kTok) + 1;
-        q.step = p.step;
-        q.more = p.more;
-    } else {
-        q.first = (min(q.n, p.max_context) + kTok - 1) / kTok;
-    }
+    const int rows = min(q.fresh, p.max_q) * p.heads;
+    q.units = rows <= p.unit_rows ? 1 : p.unit_shift == 0 ? 2 : ((rows - 1) >> p.unit_shift) + 1;
+    q.first = p.causal ? (int)((q.n - q.fresh + 2ll + p.slack + kTok - 1) >> 6) + 1
+                       : (min(q.n, p.max_context) + kTok - 1) >> 6;
     return q;
 }
 
@@ -125,8 +132,7 @@ struct Part {
     int32_t seq;
     int32_t row;          // first query row of the unit, over the whole call
     int32_t rows;         // its rows
-    int32_t token;        // first row's index within the sequence's rows
-    int32_t ahead;        // tokens before the sequence's first new one
+    int32_t ahead, rest;  // first row: context before its token; its head
     int32_t context;      // tokens of the sequence that may be seen
     int32_t t0, t1;       // tiles
     int32_t tiles;        // of the whole unit
@@ -135,7 +141,7 @@ struct Part {
     // tokens that row r of the unit sees
     PA_DEVICE int32_t seen(const Params& p, int r) const {
         if (r >= rows) return 0;
-        return p.causal ? min(ahead + (token + r) / p.heads + 1, context) : context;
+        return p.causal ? min(ahead + (int)(((rest + r) * p.per_head) >> 16) + 1, context) : context;
     }
 };
 
@@ -143,7 +149,16 @@ struct Line {
     int64_t at, end;      // what is left of the stretch
     int64_t unit_at;      // place of unit u of sequence s on the line
     int32_t s, u;
+    int32_t extra, left;  // tiles of unit u past `first`, units until there are more
+    int32_t token, rest;  // of unit u's first row
     Seq q;
+
+    // to the first unit of sequence q
+    PA_DEVICE void begin(const Params& p, const Seq& seq) {
+        q = seq;
+        u = extra = token = rest = 0;
+        left = p.step;
+    }
 };
 
 // The next share of the stretch, skipping places that the line holds too many.
@@ -151,22 +166,31 @@ PA_DEVICE bool next_part(const Params& p, Line& l, Part& w) {
     while (l.at < l.end) {
         if (l.u >= l.q.units) {
             if (++l.s >= p.seqs) return false;
-            l.q = read_seq(p, l.s, false);
-            l.u = 0;
+            l.begin(p, read_seq(p, l.s, false));
             continue;
         }
-        const int u = l.u++;
         const int64_t begin = l.unit_at;
-        l.unit_at = begin + l.q.first + (l.q.step == 0 ? 0 : l.q.more * (u / l.q.step));
+        l.unit_at = begin + l.q.first + l.extra;
+        const int r0 = l.u * p.unit_rows;
+        w.ahead = l.q.n - l.q.fresh + l.token;
+        w.rest = l.rest;
+        ++l.u;
+        l.token += p.unit_tokens;
+        l.rest += p.unit_rest;
+        if (l.rest >= p.heads) {
+            l.rest -= p.heads;
+            ++l.token;
+        }
+        if (p.causal && --l.left == 0) {
+            l.extra += p.more;
+            l.left = p.step;
+        }
         if (l.at >= l.unit_at) continue;
-        const int r0 = u * p.unit_rows;
         w.seq = l.s;
         w.row = l.q.start * p.heads + r0;
         w.rows = min(p.unit_rows, min(l.q.fresh, p.max_q) * p.heads - r0);
-        w.token = r0;
-        w.ahead = l.q.n - l.q.fresh;
         w.context = min(l.q.n, p.max_context);
-        w.tiles = (w.seen(p, w.rows - 1) + kTok - 1) / kTok;
+        w.tiles = (w.seen(p, w.rows - 1) + kTok - 1) >> 6;
         w.t0 = (int)(l.at - begin);
         w.t1 = (int)min((int64_t)w.tiles, l.end - begin);
         w.unit_at = begin;
@@ -180,14 +204,14 @@ PA_DEVICE bool next_part(const Params& p, Line& l, Part& w) {
 // scratch is shared memory.
 struct Scan {
     int64_t sums[8];
+    int64_t per;          // tiles of a stretch
     Line line;
     Part part;
     int32_t some;
 };
 
 template <int THREADS>
-PA_DEVICE bool find_stretch(const Params& p, int group, bool report, Scan& sc, Line& line, Part& part,
-                            int64_t& per) {
+PA_DEVICE void find_stretch(const Params& p, int group, bool report, Scan& sc) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the line's length, then the sequence in which this stretch begins: each
     // thread adds up an equal run of sequences, and the one whose run holds the
@@ -195,10 +219,11 @@ PA_DEVICE bool find_stretch(const Params& p, int group, bool report, Scan& sc, L
     if (threadIdx.x == 0) sc.some = 0;
     const int run = (p.seqs + THREADS - 1) / THREADS;
     const int s0 = min(p.seqs, (int)threadIdx.x * run), s1 = min(p.seqs, s0 + run);
+    Seq q;
     int64_t mine = 0;
     for (int s = s0; s < s1; ++s) {
-        const Seq q = read_seq(p, s, report);
-        mine += q.before(q.units);
+        q = read_seq(p, s, report);
+        mine += q.before(p, q.units);
     }
     int64_t upto = mine;
 #pragma unroll
@@ -215,35 +240,46 @@ PA_DEVICE bool find_stretch(const Params& p, int group, bool report, Scan& sc, L
         total += sc.sums[w];
     }
     const int64_t sum = total + p.groups - 1;
-    per = sum <= INT32_MAX ? (int64_t)((uint32_t)sum / (uint32_t)p.groups) : sum / p.groups;
+    int64_t per = sum <= INT32_MAX ? (int64_t)((uint32_t)sum / (uint32_t)p.groups) : sum / p.groups;
     per = max(per, (int64_t)p.min_tiles);
-    line.at = min(total, group * per);
-    line.end = min(total, line.at + per);
+    const int64_t at = min(total, group * per), end = min(total, at + per);
     ahead += upto - mine;
-    if (line.at < line.end && ahead <= line.at && line.at < ahead + mine) {
+    if (at < end && ahead <= at && at < ahead + mine) {
+        Line line;
+        line.at = at;
+        line.end = end;
         line.s = s0;
         line.unit_at = ahead;
-        line.q = read_seq(p, s0, false);
-        for (int64_t all; line.at >= line.unit_at + (all = line.q.before(line.q.units));) {
-            line.unit_at += all;
-            line.q = read_seq(p, ++line.s, false);
+        if (run > 1) {
+            q = read_seq(p, s0, false);
+            for (int64_t all; at >= line.unit_at + (all = q.before(p, q.units));) {
+                line.unit_at += all;
+                q = read_seq(p, ++line.s, false);
+            }
         }
-        const int64_t off = line.at - line.unit_at;
-        int u = 0, hi = line.q.units - 1;  // last unit that begins at or before `at`
-        while (u < hi) {
-            const int mid = (int)(((unsigned)u + hi + 1) >> 1);
-            if (line.q.before(mid) <= off) u = mid; else hi = mid - 1;
+        line.begin(p, q);
+        if (q.units > 1) {
+            const int64_t off = at - line.unit_at;
+            int u = 0, hi = q.units - 1;   // last unit that begins at or before `at`
+            while (u < hi) {
+                const int mid = (int)(((unsigned)u + hi + 1) >> 1);
+                if (q.before(p, mid) <= off) u = mid; else hi = mid - 1;
+            }
+            const int r0 = u * p.unit_rows;
+            line.unit_at += q.before(p, u);
+            line.u = u;
+            line.token = r0 / p.heads;
+            line.rest = r0 - line.token * p.heads;
+            if (p.causal) {
+                line.extra = p.more * (u / p.step);
+                line.left = p.step - u % p.step;
+            }
         }
-        line.u = u;
-        line.unit_at += line.q.before(u);
-        sc.some = next_part(p, line, part);
+        sc.per = per;
+        sc.some = next_part(p, line, sc.part);
         sc.line = line;
-        sc.part = part;
     }
     __syncthreads();
-    line = sc.line;
-    part = sc.part;
-    return sc.some != 0;
 }
 
 // Asks for the rows behind this unit's, the next unit's queries, in L2: the stretch goes

@@ -95,28 +95,31 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const uint32_t rank = tc::cluster_rank();
     const int group = blockIdx.x >> 1;
 
-    if (threadIdx.x == 0) {
-        mbar_init(&bars->q_full, 1);
-        mbar_init(&bars->q_empty, 1);
-        mbar_init(&bars->o_free, 8);           // softmax warps of both CTAs
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&bars->k_full[i], 1);
-            mbar_init(&bars->k_empty[i], 1);
-            mbar_init(&bars->v_full[i], 1);
-            mbar_init(&bars->v_empty[i], 1);
+    if (warp == 0) {
+        if (lane < 4) {
+            mbar_init(&bars->k_full[lane], 1);
+            mbar_init(&bars->k_empty[lane], 1);
+            mbar_init(&bars->v_full[lane], 1);
+            mbar_init(&bars->v_empty[lane], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->s_full[i], 1);
-            mbar_init(&bars->p_full[i], 8);
-            mbar_init(&bars->pv_done[i], 1);
+        if (lane < kInfo) mbar_init(&bars->info[lane], 1);
+        if (lane < kUnits) mbar_init(&bars->unit_info[lane], 1);
+        if (lane < 2) {
+            mbar_init(&bars->s_full[lane], 1);
+            mbar_init(&bars->p_full[lane], 8);
+            mbar_init(&bars->pv_done[lane], 1);
         }
-        for (int i = 0; i < kInfo; ++i) mbar_init(&bars->info[i], 1);
-        for (int i = 0; i < kUnits; ++i) mbar_init(&bars->unit_info[i], 1);
-        bars->abort = 0;
+        if (lane == 0) {
+            mbar_init(&bars->q_full, 1);
+            mbar_init(&bars->q_empty, 1);
+            mbar_init(&bars->o_free, 8);       // softmax warps of both CTAs
+            bars->abort = 0;
+            tc::prefetch_tmap(&tmap_q);
+            tc::prefetch_tmap(&tmap_k);
+            tc::prefetch_tmap(&tmap_v);
+        }
         fence_mbar_init();
-        tc::prefetch_tmap(&tmap_q);
-        tc::prefetch_tmap(&tmap_k);
-        tc::prefetch_tmap(&tmap_v);
+        __syncwarp();
     }
     if (warp == 1) {
         tc::tmem_alloc2(&bars->tmem_base, 512);
@@ -125,10 +128,7 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     griddep_wait();
     griddep_launch();
 
-    int64_t per;
-    Line line;
-    Part w;
-    const bool some = find_stretch<kPairThreads>(p, group, blockIdx.x == 0, bars->scan, line, w, per);
+    find_stretch<kPairThreads>(p, group, blockIdx.x == 0, bars->scan);
     tc::fence_before_sync();
     tc::cluster_sync();
     tc::fence_after_sync();
@@ -147,6 +147,9 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             }
             __syncwarp();
         };
+        Line line = bars->scan.line;
+        Part w = bars->scan.part;
+        const bool some = bars->scan.some;
         int unit = 0;
         for (; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
             tell(unit, w.t1 - w.t0);
@@ -204,6 +207,9 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int size = 1 << sl.log2_size;
         bool ok = true;
         uint32_t it = 0;
+        Line line = bars->scan.line;
+        Part w = bars->scan.part;
+        const bool some = bars->scan.some;
         for (int unit = 0; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
             int32_t next = sl.fetch(w, table, w.t0);
@@ -306,6 +312,10 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // limit, so none may stay away)
         bool ok = true;
         int32_t chain_rows = 0, chain_row = 0, chain = 0;
+        Line line = bars->scan.line;
+        Part w = bars->scan.part;
+        const bool some = bars->scan.some;
+        const int64_t per = bars->scan.per;
         for (int unit = 0; unit == 0 ? some : next_part(p, line, w); ++unit) {
             const int ur = r + 64 * (int)rank;         // row of the unit
             const int lim = w.seen(p, ur), ctx = w.seen(p, w.rows - 1);  // tokens that this row sees, and the last
