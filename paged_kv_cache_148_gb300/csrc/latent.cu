@@ -259,6 +259,9 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     tc::tma_load_2d(smem + L::kRope + slot * kBlock + lane * box * 128, &tmap_rope,
                                     kDim, row, bar);
                 ++rope_n;
+                if (next >= 0 && next < p.num_blocks)  // the next tile, which waits for its slots
+                    ask_rows(p, (next << p.log2_bp) + (((t + 1) * kTok + lane * box) & (bp - 1)), box, (kDim + p.rope_dim) * 2);
+                __syncwarp();
                 if (t == w.t0 && unit > 0) {  // Q behind the unit's first tile: it waits for the unit before
                     if (!(ok = wait_warp(&bars->q_empty, (unit - 1) & 1, bars, p.d_err))) break;
                     load_q();
@@ -802,6 +805,7 @@ static pa_status attention(const pa_latent_pool* pool, const void* q, int32_t he
         return PA_ERR_INVALID_ARG;
     Params p;
     p.q = (const char*)q;
+    p.rows = (const char*)pool->rows;
     p.num_blocks = pool->num_blocks;
     p.log2_bp = ilog2(pool->block_size);
     p.latent_dim = pool->latent_dim;

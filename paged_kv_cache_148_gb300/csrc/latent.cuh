@@ -27,7 +27,7 @@ constexpr int kInfo = 8;
 constexpr int kUnits = 4;
 
 struct Params {
-    const char* q;
+    const char *q, *rows;
     int32_t num_blocks, log2_bp, latent_dim, rope_dim;
     int32_t heads;
     const int32_t *starts, *lens, *tables;  // starts: null for one query a sequence
@@ -280,6 +280,18 @@ PA_DEVICE void find_stretch(const Params& p, int group, bool report, Scan& sc) {
         sc.line = line;
     }
     __syncthreads();
+}
+
+// Asks for rows of a tile ahead in L2.  The rings hold two tiles, too few to cover the
+// latency of HBM.  The requests go through the TMA unit, a page an instruction (by the
+// prefetches of a warp's own loads the issuing warps lost a third of their pace), and
+// tiles too far ahead cost more than they save.  Eight contexts of 100K tokens:
+// the one-CTA kernel on 64 heads 172.8 us without, 161.6, 160.6, 169.3, 182.7 one to
+// four tiles ahead (on 16 heads 155.7; 149.4, 149.9, 158.1, 170.3); the pair kernel on
+// 128 heads 207 us, 198.6, 198.8, 199.1, 203.8, 214.7 with 2, 3, 4, 6, 8.
+PA_DEVICE void ask_rows(const Params& p, int row, int rows, int row_bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                 ::"l"(p.rows + (int64_t)row * row_bytes), "r"(rows * row_bytes) : "memory");
 }
 
 // Asks for the rows behind this unit's, the next unit's queries, in L2: the stretch goes

@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kPairThreads = 256;
 constexpr int kPairBars = 2048;
+constexpr int kPairAhead = 3;        // tiles
 
 template <int NJ>  // 256 dims each
 struct PairLayout {
@@ -212,10 +213,11 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const bool some = bars->scan.some;
         for (int unit = 0; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
-            int32_t next = sl.fetch(w, table, w.t0);
+            int32_t next = sl.fetch(w, table, w.t0), ahead = sl.fetch(w, table, w.t0 + kPairAhead);
             for (int t = w.t0; t < w.t1; ++t, ++it) {
-                const int32_t id = next;
+                const int32_t id = next, far = ahead;
                 next = sl.fetch(w, table, t + 1);
+                ahead = sl.fetch(w, table, t + kPairAhead + 1);
                 int row;
                 const bool live = sl.row(id, t, nullptr, row);
                 const uint32_t mask = __ballot_sync(0xffffffffu, live);
@@ -229,6 +231,9 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     tc::tma2_load_5d(smem + L::kV + slot * L::kVBytes + ((lane << sl.log2_size) >> 3) * (NJ * 2048),
                                      &tmap_v, 0, 0, 2 * (int)rank, 0, row >> 3,
                                      tc::cluster_addr(&bars->v_full[slot], rank));
+                if (sl.row(far, t + kPairAhead, nullptr, row) && (uint32_t)((lane << sl.log2_size) >> 5) == rank)
+                    ask_rows(p, row, size, L::kBlocks * 128);
+                __syncwarp();
             }
         }
         __syncwarp();
