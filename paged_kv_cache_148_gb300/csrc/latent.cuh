@@ -6,7 +6,7 @@
 
 #include "host_common.h"
 #include "rope.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_pair.cuh"
 
 namespace pa {
 namespace lat {
