@@ -199,7 +199,6 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const bool some = bars->scan.some;
         int unit = 0;
         for (; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
-            tell(unit, w.t1 - w.t0);
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
             auto fetch = [&](int t) -> int32_t {     // this lane's page of tile t; -1 past the end
                 const int64_t pos = (int64_t)t * kTok + lane * box;
@@ -208,15 +207,15 @@ latent_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 return e < p.max_blocks ? max(__ldg(table + e), -1) : p.num_blocks;
             };
             auto load_q = [&] {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&bars->q_full, (2 * PAIRS + 1) * R * 128);
-                    for (int b = 0; b <= 2 * PAIRS; ++b)
-                        tc::tma_load_2d(smem + b * R * 128, &tmap_q, b * 64, w.row, &bars->q_full);
-                }
+                if (lane == 0) mbar_arrive_expect_tx(&bars->q_full, (2 * PAIRS + 1) * R * 128);
+                __syncwarp();
+                if (lane <= 2 * PAIRS)
+                    tc::tma_load_2d(smem + lane * R * 128, &tmap_q, lane * 64, w.row, &bars->q_full);
                 __syncwarp();
                 ++q_n;
             };
             int32_t next = fetch(w.t0);
+            tell(unit, w.t1 - w.t0);
             if (unit == 0) load_q();
             if (lane == 0) ask_next_q(p, line, w, R, (kDim + p.rope_dim) * 2);
             __syncwarp();

@@ -153,19 +153,18 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const bool some = bars->scan.some;
         int unit = 0;
         for (; ok && (unit == 0 ? some : next_part(p, line, w)); ++unit) {
-            tell(unit, w.t1 - w.t0);
             const int32_t* table = p.tables + (int64_t)w.seq * p.max_blocks;
             auto load_q = [&] {
-                if (lane == 0) {
-                    if (rank == 0) mbar_arrive_expect_tx(&bars->q_full, 2 * L::kBlocks * L::kQBlock);
-                    const uint32_t bar = tc::cluster_addr(&bars->q_full, 0);
-                    for (int b = 0; b < L::kBlocks; ++b)
-                        tc::tma2_load_2d(smem + b * L::kQBlock, &tmap_q, b * 64, w.row + 64 * (int)rank, bar);
-                }
+                if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&bars->q_full, 2 * L::kBlocks * L::kQBlock);
+                __syncwarp();
+                if (lane < L::kBlocks)
+                    tc::tma2_load_2d(smem + lane * L::kQBlock, &tmap_q, lane * 64, w.row + 64 * (int)rank,
+                                     tc::cluster_addr(&bars->q_full, 0));
                 __syncwarp();
                 ++q_n;
             };
             int32_t next = sl.fetch(w, table, w.t0);
+            tell(unit, w.t1 - w.t0);
             if (unit == 0) load_q();
             if (lane == 0 && rank == 0) ask_next_q(p, line, w, 128, L::kBlocks * 128);
             __syncwarp();
