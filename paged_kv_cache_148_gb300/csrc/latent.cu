@@ -16,10 +16,10 @@
 // fill all 512.
 //
 // Roles (224 threads, one CTA per SM):
-//   warp 0     TMA producer: Q of a unit; the tiles as boxes of one page x 64
-//              elements (128-byte swizzle) through the block table, into a
-//              ring of 128-dim pairs and a ring of rotary blocks.
-//   warp 1     issues the MMAs of S, a pair as it lands.
+//   warp 0     TMA producer: Q of a unit; the tiles as boxes of one page (at most 64
+//              tokens) through the block table, into a ring of parts and a ring
+//              of rotary blocks (128-byte swizzle); asks for the tile ahead in L2.
+//   warp 1     issues the MMAs of S, a part as it lands.
 //   warp 6     issues the MMAs of O^T, a tile when its P is there.  Two issuers,
 //              each waiting for its own operands: with one, either product waits
 //              behind the other's (a tile's slots come free only behind its O^T,
@@ -35,6 +35,18 @@
 // The running reference of a row's scores moves only when its maximum grew by
 // more than 2^16 (bf16 has float32's range, so P loses nothing by it): the
 // rescaling of O^T, which takes all four warps, is then rare.
+//
+// What bounds it.  The MMAs of a tile take 36 x 32 + 16 x 48 = 1920 cycles at 64 rows
+// (M = 64 runs at half rate, N = 64 of M = 128 is bound by shared memory), HBM at its
+// copy rate 3140: long contexts run near HBM's rate.  Eight contexts of 32K to 131K
+// tokens on 64 heads (755 MB): 136 us, 5.5 TB/s, 82 % of the copy bandwidth (ncu: DRAM
+// 1.01 x the algorithmic bytes, tensor pipe 48 % active); of 100K on 16 heads 149 us,
+// 91 %.  Short calls are bound by the way to the first product, about 8000 cycles
+// (lengths, table and rows are three loads that wait for one another, and all code is
+// cold): one context of 700 tokens takes 14.6 us.
+// On the way (us, the eight contexts above): one issuer 234, then 203 with offsets that
+// are compile-time constants, 173 with O^T and S in the order of their operands, 157
+// with two issuers, 149 without a search from unit to unit, 139 with the next tile in L2.
 #include "latent.cuh"
 
 namespace pa {
@@ -684,7 +696,9 @@ __global__ void __launch_bounds__(512) latent_merge_many_kernel(const Params p) 
 }
 
 static cudaError_t launch_merge(const Params& p, int64_t units, cudaStream_t stream) {
-    // a unit is cut into groups / units parts or so
+    // a unit is cut into groups / units parts or so: 20 of them at this border, which the
+    // first kernel reads in 23 us (eight contexts on 152 stretches) and the second in 13;
+    // for two or three parts a unit it is 14 us by the second and 9 by the first
     if (p.groups >= 6 * units) {
         // a block for every unit, not for every stretch: empty ones would cost a launch each
         const unsigned cuts = (unsigned)units;
@@ -721,6 +735,10 @@ static Shape shape_of(const pa_latent_pool* pool, int heads, int seqs, bool pref
     Shape s;
     if (max_q > total_q) max_q = total_q;
     const int64_t rows = (int64_t)max_q * heads;   // most of a sequence
+    // units of two times 64 rows where there are more than 64 (64 contexts of 128 to 4096
+    // tokens on 65, 96, 128 heads: 55, 56, 59 us, by units of 64 rows 81, 80, 84; 5 drafted
+    // tokens on 16 heads 52 and 68; at 64 rows the one-CTA kernel takes 161 us for eight
+    // contexts of 100K, pairs with half their rows empty as long as for 128, 199)
     s.pair = rows > 64 && pool->rope_dim == 64 && pool->latent_dim % 256 == 0;
     if (s.pair) {
         s.unit_rows = s.R = 128;

@@ -23,8 +23,9 @@ constexpr int kInfo = 8;
 // know no more of units: with the search for them in their loops the compiler loses
 // track of what is uniform in the warp, and an MMA with descriptors from general
 // registers takes 40 to 100 cycles to issue, against 24 to 64 to run.  The producer is
-// at most two units ahead of them (Q has one buffer).
-constexpr int kUnits = 4;
+// two units ahead of S's issuer at most (Q has one buffer), S two tiles ahead of the
+// softmax, which ends a unit when its O is done: four units at the most in all.
+constexpr int kUnits = 8;
 
 struct Params {
     const char *q, *rows;
