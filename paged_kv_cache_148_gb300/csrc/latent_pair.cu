@@ -18,13 +18,12 @@
 //
 // What bounds it.  The MMAs of a tile take 36 x 25.5 + 8 x 64.5 = 1434 cycles for 128
 // rows (S reads 3 KB of shared memory an MMA and SM; O runs at the tensor core's
-// rate), 717 a CTA, where the one-CTA kernel takes 1920.  A tile takes about 1700
+// rate), 717 a CTA, where the one-CTA kernel takes 1920.  A tile takes about 1500
 // with its operands in L2, and 6500 more stand between two units (the epilogue takes
 // the softmax warps, Q has one buffer).  16 x 512 queries of 32 heads behind 2048
-// tokens: 1.03 ms, 1.28 PFLOP/s, 69 % of the measured bf16 rate (ncu: tensor pipe 59 %
-// active, L2 hits 89 %).  Decoding on 128 heads HBM's latency shows, with two slots
-// a ring: eight contexts of 100K tokens 199 us, 68 % of the copy bandwidth.
-// K in two separately released parts was no faster (1060 us against 1035).
+// tokens: 0.94 ms, 1.40 PFLOP/s, 75 % of the measured bf16 rate.  Decoding on 128 heads
+// the softmax's own path shows: eight contexts of 100K tokens 178 us, 76 % of the copy
+// bandwidth.  K in two separately released parts was no faster (1060 us against 1035).
 #include "latent.cuh"
 
 namespace pa {
@@ -263,11 +262,14 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 if (!(ok = wait_warp(&bars->k_full[slot], phase, bars, p.d_err))) break;
                 tc::fence_after_sync();
                 const uint32_t d = tmem + 32u * (it & 1);
-                const uint64_t b = dk + (uint64_t)(slot * (L::kKBytes >> 4));
+                if (tc::elected()) {
+                    const uint32_t a = (uint32_t)dq, b = (uint32_t)dk + slot * (L::kKBytes >> 4);
 #pragma unroll
-                for (int k = 0; k < 4 * L::kBlocks; ++k)
-                    tc::mma2_ss_warp(d, dq + (((k >> 2) * L::kQBlock + (k & 3) * 32) >> 4),
-                                     b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
+                    for (int k = 0; k < 4 * L::kBlocks; ++k)
+                        tc::mma2_ss(d, a + (((k >> 2) * L::kQBlock + (k & 3) * 32) >> 4), dq >> 32,
+                                    b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), dk >> 32, idesc, k > 0 ? 1u : 0u);
+                }
+                __syncwarp();
                 tc::commit2_warp(&bars->s_full[it & 1]);
                 tc::commit2_warp(&bars->k_empty[slot]);
                 if (t + 1 == n) tc::commit2_warp(&bars->q_empty);
@@ -292,15 +294,18 @@ latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             for (int t = 0; t < n; ++t, ++it) {
                 if (!(ok = wait_warp(&bars->p_full[it & 1], (it >> 1) & 1, bars, p.d_err))) break;
                 tc::fence_after_sync();
-                const uint64_t a = dp + (uint64_t)((it & 1) * (L::kPBytes >> 4));
-                const uint64_t b = dv + (uint64_t)(slot * (L::kVBytes >> 4));
+                const uint32_t a = (uint32_t)dp + (it & 1) * (L::kPBytes >> 4);
+                const uint32_t b = (uint32_t)dv + slot * (L::kVBytes >> 4);
                 const uint32_t first = t > 0 ? 1u : 0u;
+                if (tc::elected()) {
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc::mma2_ss_warp(tmem + 128 + 128 * j, a + (k * 32 >> 4),
-                                         b + ((j * 2048 + k * NJ * 4096) >> 4), idesc, k > 0 ? 1u : first);
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma2_ss(tmem + 128 + 128 * j, a + (k * 32 >> 4), dp >> 32,
+                                        b + ((j * 2048 + k * NJ * 4096) >> 4), dv >> 32, idesc, k > 0 ? 1u : first);
+                }
+                __syncwarp();
                 tc::commit2_warp(&bars->pv_done[it & 1]);
                 tc::commit2_warp(&bars->v_empty[slot]);
                 if (++slot == L::kSlots) slot = 0;
