@@ -736,9 +736,9 @@ static Shape shape_of(const pa_latent_pool* pool, int heads, int seqs, bool pref
     if (max_q > total_q) max_q = total_q;
     const int64_t rows = (int64_t)max_q * heads;   // most of a sequence
     // units of two times 64 rows where there are more than 64 (64 contexts of 128 to 4096
-    // tokens on 65, 96, 128 heads: 55, 56, 59 us, by units of 64 rows 81, 80, 84; 5 drafted
-    // tokens on 16 heads 52 and 68; at 64 rows the one-CTA kernel takes 161 us for eight
-    // contexts of 100K, pairs with half their rows empty as long as for 128, 199)
+    // tokens on 65, 96, 128 heads: 54, 56, 59 us, by units of 64 rows 81, 80, 84; 5 drafted
+    // tokens on 16 heads 50 and 68; at 64 rows the one-CTA kernel takes 161 us for eight
+    // contexts of 100K, pairs with half their rows empty as long as for 128, 184)
     s.pair = rows > 64 && pool->rope_dim == 64 && pool->latent_dim % 256 == 0;
     if (s.pair) {
         s.unit_rows = s.R = 128;

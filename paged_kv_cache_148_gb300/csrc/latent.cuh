@@ -289,7 +289,8 @@ PA_DEVICE void find_stretch(const Params& p, int group, bool report, Scan& sc) {
 // tiles too far ahead cost more than they save.  Eight contexts of 100K tokens:
 // the one-CTA kernel on 64 heads 172.8 us without, 161.6, 160.6, 169.3, 182.7 one to
 // four tiles ahead (on 16 heads 155.7; 149.4, 149.9, 158.1, 170.3); the pair kernel on
-// 128 heads 207 us, 198.6, 198.8, 199.1, 203.8, 214.7 with 2, 3, 4, 6, 8.
+// 128 heads 204 us, 187, 184, 185, 190, 203 with 2, 3, 4, 6, 8 (64 contexts of 128 to 4096
+// 60.0 us, 58.0, 57.1, 58.8, 60.0, 61.8).
 PA_DEVICE void ask_rows(const Params& p, int row, int rows, int row_bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
                  ::"l"(p.rows + (int64_t)row * row_bytes), "r"(rows * row_bytes) : "memory");

@@ -22,8 +22,9 @@
 // with its operands in L2, and 6500 more stand between two units (the epilogue takes
 // the softmax warps, Q has one buffer).  16 x 512 queries of 32 heads behind 2048
 // tokens: 0.94 ms, 1.40 PFLOP/s, 75 % of the measured bf16 rate.  Decoding on 128 heads
-// the softmax's own path shows: eight contexts of 100K tokens 178 us, 76 % of the copy
-// bandwidth.  K in two separately released parts was no faster (1060 us against 1035).
+// HBM's latency shows, with two slots a ring: eight contexts of 100K tokens 184 us, 74 %
+// of the copy bandwidth.  K in two separately released parts was no faster (1060 us
+// against 1035).
 #include "latent.cuh"
 
 namespace pa {
